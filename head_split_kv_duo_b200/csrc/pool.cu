@@ -13,37 +13,14 @@
 // duo_pool_decode_step appends one token to each listed sequence on each listed layer
 // (one launch) and attends for all of them (one launch of the tcgen05 decode kernel
 // over every (layer, sequence, KV head) item).
-#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
-#include <vector>
 
 #include "decode_merge.cuh"
 #include "tcgen05.cuh"
 #include "nvtx_range.h"
-
-struct duo_pool {
-  int layers = 0, Hkv = 0, Hq = 0, G = 0, D = 0, S = 0, W = 0, max_seqs = 0, pages_per_seq = 0;
-  int64_t num_pages = 0, max_len = 0;
-  float scale = 0.f;
-  char *buf = nullptr;
-  size_t bytes = 0;
-  bool initialised = false;
-  int num_sms = 0;
-  uint32_t *status = nullptr;
-  uint32_t *counters = nullptr;  // one ticket per item of a call
-  float *partials = nullptr;     // (max CTAs + items) segments of G partial rows
-  int max_items = 0;
-  duo::PoolLayerDesc *d_layers = nullptr;
-  int *d_table = nullptr;
-  std::vector<duo::PoolLayerDesc> h_layers;
-  std::vector<int> hr, hs;
-  std::vector<int> free_pages;                 // stack of free physical pages
-  std::vector<uint8_t> open;                   // per slot
-  std::vector<std::vector<int>> pages;         // per slot: physical page of each logical page
-  std::vector<std::vector<int64_t>> len;       // per slot, per layer
-};
+#include "pool_internal.h"
 
 namespace duo {
 
@@ -231,9 +208,7 @@ cudaError_t launch_pool_chunk_append(const PoolChunkAppend &c, int Hr, int /*Hs*
 
 }  // namespace duo
 
-using namespace duo;
-
-namespace {
+namespace duo {
 
 // First use: clear the buffer, describe every layer (tensor maps encoded on the host)
 // and copy the descriptions to the device.
@@ -284,7 +259,13 @@ duo_status pool_init(duo_pool *P, cudaStream_t st) {
   return DUO_OK;
 }
 
-bool seq_ok(const duo_pool *P, int seq) { return P && seq >= 0 && seq < P->max_seqs && P->open[seq]; }
+}  // namespace duo
+
+using namespace duo;
+
+namespace {
+
+bool seq_ok(const duo_pool *P, int seq) { return P && P->is_open(seq); }
 
 }  // namespace
 
@@ -359,7 +340,8 @@ duo_status duo_pool_create(int layers, int kv_heads, int head_dim, const uint8_t
     D.sv = P->buf + L.sv[l];
   }
   P->free_pages.reserve(static_cast<size_t>(num_pages));
-  for (int64_t pg = num_pages - 1; pg >= 0; --pg) P->free_pages.push_back(static_cast<int>(pg));
+  for (int64_t pg = 0; pg < num_pages; ++pg) P->free_pages.push_back(static_cast<int>(pg));  // a heap as it is
+  P->refs.assign(static_cast<size_t>(num_pages), 0);
   P->open.assign(max_seqs, 0);
   P->pages.assign(max_seqs, {});
   P->len.assign(max_seqs, std::vector<int64_t>(layers, 0));
@@ -398,7 +380,7 @@ duo_status duo_pool_open(duo_pool *P, void *stream, int *seq) {
 
 duo_status duo_pool_close(duo_pool *P, int seq) {
   if (!seq_ok(P, seq)) return DUO_ERR_INVALID;
-  for (int pg : P->pages[seq]) P->free_pages.push_back(pg);
+  for (int pg : P->pages[seq]) P->drop_page(pg);
   P->pages[seq].clear();
   P->open[seq] = 0;
   return DUO_OK;
@@ -455,15 +437,12 @@ duo_status duo_pool_append_kv(duo_pool *P, int layer, int seq, const void *k, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   duo_status r = pool_init(P, st);
   if (r != DUO_OK) return r;
-  // pages opened by this call come off the free stack; they go back if a launch fails
+  // pages opened by this call come off the free pages; they go back if a launch fails
   std::vector<int> &pg = P->pages[seq];
-  for (int64_t i = have; i < need; ++i) {
-    pg.push_back(P->free_pages.back());
-    P->free_pages.pop_back();
-  }
+  for (int64_t i = have; i < need; ++i) pg.push_back(P->take_page());
   auto undo = [&] {
     while (static_cast<int64_t>(pg.size()) > have) {
-      P->free_pages.push_back(pg.back());
+      P->drop_page(pg.back());
       pg.pop_back();
     }
   };
@@ -498,7 +477,7 @@ duo_status duo_pool_append_kv(duo_pool *P, int layer, int seq, const void *k, co
       // describes what the cache holds)
       P->len[seq][layer] = len + t0;
       while (static_cast<int64_t>(pg.size()) > (len + t0 + kPoolTile - 1) / kPoolTile) {
-        P->free_pages.push_back(pg.back());
+        P->drop_page(pg.back());
         pg.pop_back();
       }
       return DUO_ERR_CUDA;
@@ -563,8 +542,7 @@ duo_status duo_pool_decode_step(duo_pool *P, int layer0, int nlayers, int nseq, 
     const int lp = static_cast<int>(len / kPoolTile);
     int fresh = 0;
     if (lp >= static_cast<int>(P->pages[s].size())) {
-      P->pages[s].push_back(P->free_pages.back());
-      P->free_pages.pop_back();
+      P->pages[s].push_back(P->take_page());
       opened.push_back(s);
       fresh = 1;
     }
@@ -592,7 +570,7 @@ duo_status duo_pool_decode_step(duo_pool *P, int layer0, int nlayers, int nseq, 
   p.scale_log2 = P->scale * 1.4426950408889634f;
   if (launch_via_hook([&] { return launch_pool_append(ac, st); }) != cudaSuccess) {
     for (auto it = opened.rbegin(); it != opened.rend(); ++it) {  // nothing was written
-      P->free_pages.push_back(P->pages[*it].back());
+      P->drop_page(P->pages[*it].back());
       P->pages[*it].pop_back();
     }
     return DUO_ERR_CUDA;

@@ -102,6 +102,18 @@ def lib() -> ctypes.CDLL:
             L.duo_pool_append_kv.argtypes = [vp, i32, i32, vp, vp, i32, vp]
             L.duo_pool_decode_step.restype = i32
             L.duo_pool_decode_step.argtypes = [vp, i32, i32, i32, ctypes.POINTER(i32), vp, vp, vp, vp, vp, vp]
+            L.duo_pool_fork.restype = i32
+            L.duo_pool_fork.argtypes = [vp, i32, i32, vp, ctypes.POINTER(i32)]
+            L.duo_pool_copy.restype = i32
+            L.duo_pool_copy.argtypes = [vp, i32, vp, vp, ctypes.POINTER(i32)]
+            L.duo_rope_create.restype = i32
+            L.duo_rope_create.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_double), vp, i32, i32, ctypes.c_float,
+                                          ctypes.POINTER(vp)]
+            L.duo_rope_destroy.restype = None
+            L.duo_rope_destroy.argtypes = [vp]
+            L.duo_qk_norm_rope.restype = i32
+            L.duo_qk_norm_rope.argtypes = [vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float,
+                                           vp, vp, vp, vp, vp]
             L.duo_pool_page.restype = i32
             L.duo_pool_page.argtypes = [vp, i32, i32, ctypes.POINTER(i32)]
             L.duo_pool_region.restype = i32
@@ -269,6 +281,39 @@ def duo_pool_decode_step(handle, layer0, nlayers, seqs, q, k, v, out, lse, strea
     arr = (ctypes.c_int * len(seqs))(*[int(x) for x in seqs])
     return lib().duo_pool_decode_step(handle, layer0, nlayers, len(seqs), arr, _ptr(q), _ptr(k), _ptr(v), _ptr(out),
                                       _ptr(lse), _ptr(stream))
+
+
+def duo_pool_fork(handle, seq, n, stream=None):
+    """Returns (status, list of n slots)."""
+    arr = (ctypes.c_int * max(1, int(n)))()
+    st = lib().duo_pool_fork(handle, seq, n, _ptr(stream), arr)
+    return st, list(arr)
+
+
+def duo_pool_copy(handle, seq, dst_handle, stream=None):
+    s = ctypes.c_int()
+    st = lib().duo_pool_copy(handle, seq, dst_handle, _ptr(stream), ctypes.byref(s))
+    return st, s.value
+
+
+def duo_rope_create(head_dim, rot_dim, inv_freq, pair_axis=None, axes=1, interleaved=0, scale=1.0):
+    """Returns (status, handle); inv_freq and pair_axis are sequences of rot_dim / 2 numbers."""
+    f = (ctypes.c_double * len(inv_freq))(*[float(x) for x in inv_freq])
+    a = None if pair_axis is None else (ctypes.c_uint8 * len(pair_axis))(*[int(x) for x in pair_axis])
+    h = ctypes.c_void_p()
+    st = lib().duo_rope_create(head_dim, rot_dim, f, a, axes, interleaved, scale, ctypes.byref(h))
+    return st, h
+
+
+def duo_rope_destroy(handle):
+    lib().duo_rope_destroy(handle)
+
+
+def duo_qk_norm_rope(handle, n, q_heads, kv_heads, dtype, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight,
+                     eps, positions, q_out, k_out, v_out, stream=None) -> int:
+    return lib().duo_qk_norm_rope(handle, n, q_heads, kv_heads, dtype, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+                                  v_stride, _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(q_out),
+                                  _ptr(k_out), _ptr(v_out), _ptr(stream))
 
 
 def duo_pool_page(handle, seq, logical_page):
@@ -453,6 +498,13 @@ class DuoPool:
         if st != DUO_OK:
             raise DuoError(st, what)
 
+    def _stream(self, stream):
+        """The launch stream: `stream`, or the current one of the pool's device, which must be the current device."""
+        dev = self.buffer.device
+        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+            raise ValueError(f"the pool is on {dev}, which is not the current device")
+        return _stream_ptr(stream)
+
     def open(self, stream=None) -> int:
         st, s = duo_pool_open(self.handle, _stream_ptr(stream))
         self._check(st, "duo_pool_open")
@@ -493,6 +545,20 @@ class DuoPool:
                     "duo_pool_decode_step")
         return out, lse
 
+    def fork(self, seq, n=1, stream=None):
+        """duo_pool_fork: n new sequences holding what `seq` holds; returns their slots."""
+        st, children = duo_pool_fork(self.handle, seq, n, self._stream(stream))
+        self._check(st, "duo_pool_fork")
+        return children
+
+    def copy(self, seq, to, stream=None) -> int:
+        """duo_pool_copy: `seq` into the pool `to` (which may be this one); returns its slot there."""
+        if to.buffer.device != self.buffer.device:
+            raise ValueError("copy: both pools must be on one device")
+        st, s = duo_pool_copy(self.handle, seq, to.handle, self._stream(stream))
+        self._check(st, "duo_pool_copy")
+        return s
+
     def page(self, seq, logical_page) -> int:
         st, p = duo_pool_page(self.handle, seq, logical_page)
         self._check(st, "duo_pool_page")
@@ -506,6 +572,81 @@ class DuoPool:
 
     def device_status(self, stream=None) -> int:
         return duo_pool_device_status(self.handle, _stream_ptr(stream))
+
+
+class DuoRope:
+    """Head norms and rotary positions of queries and keys (duo_qk_norm_rope): inv_freq holds
+    the angular frequency of each of rot_dim / 2 pairs (rot_dim = 2 len(inv_freq)), pair_axis
+    the position axis of each (None: one axis)."""
+
+    def __init__(self, head_dim, inv_freq, *, pair_axis=None, interleaved=False, scale=1.0):
+        self.head_dim, self.rot_dim = head_dim, 2 * len(inv_freq)
+        if pair_axis is not None and len(pair_axis) != len(inv_freq):
+            raise ValueError(f"pair_axis: expected {len(inv_freq)} entries, got {len(pair_axis)}")
+        self.axes = 1 if pair_axis is None else 1 + max(int(x) for x in pair_axis)
+        st, self.handle = duo_rope_create(head_dim, self.rot_dim, inv_freq, pair_axis, self.axes, int(bool(interleaved)),
+                                          scale)
+        if st != DUO_OK:
+            raise DuoError(st, "duo_rope_create")
+
+    def close(self):
+        if getattr(self, "handle", None):
+            duo_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _side(self, x, out, name, n, dtype, device):
+        """(stride, out) of one of q, k, v [n][heads][head_dim], its tokens any stride apart."""
+        h = x.shape[1] if x.dim() == 3 else 0
+        if x.dtype != dtype or x.device != device or h < 1 or x.shape[0] != n or x.shape[2] != self.head_dim or \
+                x.stride(2) != 1 or (h > 1 and x.stride(1) != self.head_dim):
+            raise ValueError(f"{name}: expected {dtype} [{n}][heads][{self.head_dim}] on {device}, each token's rows "
+                             f"dense, got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+        if out is None:
+            out = torch.empty((n, h, self.head_dim), dtype=dtype, device=device)
+        elif out.dtype != dtype or out.device != device or out.shape != x.shape or not out.is_contiguous():
+            raise ValueError(f"{name}_out: expected contiguous {dtype} {tuple(x.shape)} on {device}")
+        return (x.stride(0) if n > 1 else h * self.head_dim), out
+
+    def norm_rope(self, q, k, positions, v=None, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None,
+                  v_out=None, stream=None):
+        """q [n][Hq][d], k, v [n][Hkv][d] (views of packed rows will do; q, k or v may be None),
+        positions int32 [axes][n] or, of one axis, [n] -> dense (q, k, v)."""
+        x = q if q is not None else k
+        if x is None:
+            raise ValueError("q or k is needed")
+        n, dtype, device = x.shape[0], x.dtype, x.device
+        if dtype not in _DTYPES or device.type != "cuda" or device.index != torch.cuda.current_device():
+            raise ValueError(f"expected bf16 or fp32 tensors on the current CUDA device, got {dtype} on {device}")
+        if positions.dtype != torch.int32 or positions.device != device or not positions.is_contiguous() or \
+                tuple(positions.shape) not in (((self.axes, n),) if self.axes > 1 else ((1, n), (n,))):
+            raise ValueError(f"positions: expected contiguous int32 [{self.axes}][{n}] on {device}, got "
+                             f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None and (w.dtype != dtype or w.device != device or tuple(w.shape) != (self.head_dim,) or
+                                  not w.is_contiguous()):
+                raise ValueError(f"{name}: expected contiguous {dtype} [{self.head_dim}] on {device}")
+        qs = ks = vs = 0
+        if q is not None:
+            qs, q_out = self._side(q, q_out, "q", n, dtype, device)
+        if k is not None:
+            ks, k_out = self._side(k, k_out, "k", n, dtype, device)
+        if v is not None:
+            vs, v_out = self._side(v, v_out, "v", n, dtype, device)
+        if k is not None and v is not None and k.shape[1] != v.shape[1]:
+            raise ValueError("k and v: expected as many heads")
+        kv = k if k is not None else v
+        st = duo_qk_norm_rope(self.handle, n, 0 if q is None else q.shape[1], 0 if kv is None else kv.shape[1],
+                              _DTYPES[dtype], q, qs, k, ks, v, vs, q_weight, k_weight, eps, positions, q_out, k_out,
+                              v_out, _stream_ptr(stream))
+        if st != DUO_OK:
+            raise DuoError(st, "duo_qk_norm_rope")
+        return q_out, k_out, v_out
 
 
 def gated_attention(q, k, v, alpha, S, W, softmax_scale=0.0, out=None, stream=None):

@@ -277,9 +277,11 @@ DUO_API duo_status duo_decode_attention_static_scratch(duo_cache *cache, int lay
  * Streaming heads keep their sinks + ring per sequence slot, [slot][H_s][S+W][d], with
  * the slot rule of duo_append_kv.  The host keeps every sequence's length per layer.
  * bf16, head_dim 128, retrieval format DUO_KV_SAME, at most 16 query heads per KV head
- * (else DUO_ERR_UNSUPPORTED).  Sequences are filled with duo_pool_append_kv and decoded
- * with duo_pool_decode_step; pre-fill attention over a pool is not provided.  Calls on
- * one pool must be ordered on one stream.  Errors follow the cache's contract: checked
+ * (else DUO_ERR_UNSUPPORTED).  Sequences are filled with duo_pool_append_kv or, with
+ * attention, duo_pool_prefill, decoded with duo_pool_decode_step, branched with
+ * duo_pool_fork and moved with duo_pool_copy.  Free pages are handed out lowest first.
+ * Calls on one pool must be ordered on one stream; a call's launches carry the lengths and
+ * pages of the moment it was made, so a captured graph repeats that call and no other.  Errors follow the cache's contract: checked
  * before any launch, lengths follow what the cache holds.
  */
 typedef struct duo_pool duo_pool;
@@ -331,6 +333,30 @@ DUO_API duo_status duo_pool_decode_step(duo_pool *pool, int layer0, int nlayers,
                                         const void *q, const void *k, const void *v, void *out, float *lse,
                                         void *cuda_stream);
 
+/*
+ * Forks a sequence: n >= 1 (at most 128) new sequences that hold the same tokens on every
+ * layer.  Pages that are full on every layer are shared -- listed by parent and children
+ * alike, returned when the last of them closes -- and the pages behind them (one, when
+ * the layers are equally long; none at a multiple of 128) as well as the sinks and rings
+ * of streaming heads are copied, each child its own.  Parent and children then go on
+ * independently: append, decode, fork again, close in any order.  (A ring cannot be rolled
+ * back, what it evicted is gone: drafts that may be dropped go into a fork.)  One launch
+ * for up to about 700 / (n + 1) copied pages.  children[n] receives the slots, the lowest
+ * free ones in order.  DUO_ERR_CAPACITY without n free slots or enough free pages; on any
+ * error no sequence changes.
+ */
+DUO_API duo_status duo_pool_fork(duo_pool *pool, int seq, int n, void *cuda_stream, int *children);
+
+/*
+ * Copies a sequence of `src` into a free slot of `dst` (*new_seq), sharing nothing: to a
+ * pool of another size (other max_seqs, max_len, num_pages), or within one pool
+ * (dst == src).  Both pools must agree in layers, KV heads, retrieval heads, S and W
+ * (else DUO_ERR_INVALID) and be on the same device; calls on both must be ordered with
+ * `cuda_stream`.  DUO_ERR_CAPACITY without a free slot or enough free pages in dst, or
+ * when the sequence is longer than its max_len; on any error no sequence changes.
+ */
+DUO_API duo_status duo_pool_copy(const duo_pool *src, int seq, duo_pool *dst, void *cuda_stream, int *new_seq);
+
 /* Physical page of a sequence's logical page (host bookkeeping, for inspection). */
 DUO_API duo_status duo_pool_page(const duo_pool *pool, int seq, int logical_page, int *physical_page);
 /* Device address and size of a layer's page array (DUO_REGION_RETR_K / _V,
@@ -338,6 +364,52 @@ DUO_API duo_status duo_pool_page(const duo_pool *pool, int seq, int logical_page
 DUO_API duo_status duo_pool_region(const duo_pool *pool, int layer, duo_region which, void **ptr, uint64_t *bytes);
 /* Synchronises `cuda_stream`, reads and clears the pool's device status word. */
 DUO_API duo_status duo_pool_device_status(duo_pool *pool, void *cuda_stream);
+
+/*
+ * ---- Norms and positions of queries and keys ----
+ *
+ * The attention calls take queries and keys as the model attends with them.  This pass
+ * makes them from the projection's rows: an RMS norm of each head and the rotary position
+ * rotation of queries and keys, with the values copied along, so that packed projection
+ * output becomes the dense q, k and v of the append, pre-fill and decode calls in one
+ * launch.  A handle holds the rotation (host metadata only):
+ *   head_dim     64 or 128
+ *   rot_dim      rotated elements of a head, a multiple of 16 up to head_dim; elements from
+ *                rot_dim on are not rotated
+ *   inv_freq     host [rot_dim / 2], angular frequency of each pair in radians per
+ *                position, 0 .. 1e6 (any scaling of long contexts is already in it)
+ *   pair_axis    host [rot_dim / 2], position axis of each pair (time, height, width, ...),
+ *                < axes, or NULL (all 0); axes 1 .. 8
+ *   interleaved  0: pair i is elements i and i + rot_dim / 2; 1: elements 2i and 2i + 1
+ *   scale        finite, > 0: multiplies the rotated elements (1 for none)
+ */
+typedef struct duo_rope duo_rope;
+DUO_API duo_status duo_rope_create(int head_dim, int rot_dim, const double *inv_freq, const uint8_t *pair_axis,
+                                   int axes, int interleaved, float scale, duo_rope **out);
+DUO_API void duo_rope_destroy(duo_rope *rope); /* NULL is a no-op */
+
+/*
+ * For n >= 1 tokens: y = x * rsqrt(mean(x^2) + eps) * weight per head row (or y = x where
+ * that side's weight is NULL), then each pair (a, b) of y, at angle
+ * t = positions[pair_axis[i]][token] * inv_freq[i], becomes
+ * scale * (a cos t - b sin t, a sin t + b cos t).  fp32 arithmetic, one rounding at the
+ * store; angles are reduced exactly, so positions may be any int32.
+ *   q, k, v      device [n][heads][head_dim] in dtype, rows of one token dense, tokens
+ *                *_stride elements apart (>= heads * head_dim; a multiple of 16 bytes);
+ *                q_heads heads in q, kv_heads in k and v; q or k may be NULL (not both),
+ *                v may be NULL; values are copied as they are
+ *   *_weight     device [head_dim] in dtype, or NULL; eps > 0 where there is one
+ *   positions    device [axes][n] int32
+ *   *_out        device [n][heads][head_dim], NULL exactly where the input is.  Each may be
+ *                its own input when that is dense; any other overlap with the call's
+ *                tensors is DUO_ERR_INVALID.
+ * All but positions 16-byte aligned.
+ */
+DUO_API duo_status duo_qk_norm_rope(const duo_rope *rope, int n, int q_heads, int kv_heads, duo_dtype dtype,
+                                    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                    int64_t v_stride, const void *q_weight, const void *k_weight, float eps,
+                                    const int32_t *positions, void *q_out, void *k_out, void *v_out,
+                                    void *cuda_stream);
 
 /*
  * Gated mixed attention of the identification phase ("Gate Parameterization"): over
