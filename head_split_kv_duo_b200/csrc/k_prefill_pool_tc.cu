@@ -1,0 +1,552 @@
+// k_prefill_pool_tc.cu -- ragged pre-fill attention over the paged pool on the tcgen05
+// tensor cores (bf16 in, fp32 accumulate, head_dim 128, up to 16 query heads per KV head).
+//
+// The n_s new tokens of each listed sequence s, at positions len_s .. len_s+n_s-1, attend
+// ("Chunked Pre-filling", masks of "The Full and Streaming Attention Masks"), scale c:
+//   out_i = sum_j p_ij v_j / l_i,  p_ij = exp(c q_i.k_j - m_i),  l_i = sum_j p_ij
+//   over  j <= i (retrieval heads),  j <= i and (j < S or i - j < W) (streaming heads)
+// with the sums taken in one pass over tiles of 128 keys: a running reference m, and O and
+// l rescaled when a row's maximum passes it by 2^8.  Keys come straight from where they
+// are: the sequence's pages (one page = one tile), its sinks and ring slots in slot order
+// (the softmax does not ask for an order; masks say which slot holds a visible position),
+// and the call's own k and v.  The cache is only read; the append is a later launch.
+//
+// One CTA = two 128-row query tiles of one (sequence, KV head) -- a row is one of G query
+// heads at one of 128 / G consecutive positions (rows past G * (128 / G) idle) -- sharing
+// every K/V tile; 12 warps:
+//   warp 0      TMA: both Q tiles, then the K ring (2 stages)
+//   warp 1      owns TMEM; lane 0 issues every tcgen05.mma
+//   warp 2      the V ring (2 stages); by TMA, but the last tile of a chunk row by row:
+//               rows behind it belong to the next sequence, and 0 * NaN would carry a
+//               broken neighbour's values over, so they are written as zeros
+//   warps 4-7 and 8-11  softmax of query tile 0 and 1, one thread per row
+// TMEM: S_t at 128 t (P_t, bf16 pairs, over its first 64 columns), O_t at 256 + 128 t.
+// The MMA thread issues PV_0(j), S_0(j+1), PV_1(j), S_1(j+1): one tile's products run
+// while the other tile's softmax works.  MMAs of one thread complete in order, so S_t(j+1)
+// overwrites P_t(j) after PV_t(j) has read it, and once S_t(j) has landed O_t may be
+// rescaled in place.
+//
+// Few rows over a long history would leave most SMs idle: then a CTA's keys are split
+// into segments, each a CTA that leaves unnormalised rows, max and sum in the scratch; the
+// append launch that follows joins them.
+//
+// Every mbarrier wait is bounded; one that runs out latches kDevTimeout, and every role
+// drains and exits.
+#include "pool_internal.h"
+#include "tcgen05.cuh"
+
+namespace duo {
+
+namespace {
+
+constexpr int kBM = 128, kBN = 128, kD = 128, kQT = 2;
+constexpr int kSoftWarp0 = 4;
+constexpr int kThreads = 32 * (kSoftWarp0 + 4 * kQT);
+constexpr int kKStages = 2, kVStages = 2;
+constexpr int kTile = 32768;  // bytes of a 128-row operand tile: two 128B-swizzled [128][64] halves
+constexpr int kHalf = 16384;
+
+constexpr int kSmQ = 0, kSmK = kSmQ + kQT * kTile, kSmV = kSmK + kKStages * kTile, kSmBar = kSmV + kVStages * kTile;
+constexpr int kSmMisc = kSmBar + 256;
+constexpr int kSmemAlloc = kSmMisc + 256 + 1024;  // slack for aligning the base to 1 KiB
+constexpr int kTmS = 0, kTmO = 256;
+
+constexpr int kBarQ = 0, kBarKFull = 1, kBarKEmpty = kBarKFull + kKStages, kBarVFull = kBarKEmpty + kKStages,
+              kBarVEmpty = kBarVFull + kVStages, kBarSFull = kBarVEmpty + kVStages, kBarPFull = kBarSFull + kQT,
+              kBarOFull = kBarPFull + kQT, kBarDrain = kBarOFull + kQT, kNumBars = kBarDrain + 1;
+static_assert(kNumBars * 8 <= 256 && kSmemAlloc <= 227 * 1024, "shared memory");
+
+enum Source { kPages, kSlots, kChunk };
+
+// A run of consecutive key tiles of one source.
+struct Run {
+  int src, first, count;
+};
+struct Tile {
+  int src, y;  // source, first row
+};
+
+// What a CTA works on, the same in every thread.
+struct Work {
+  int s, g, idx, retr;  // listed sequence, KV head, its index among heads of its kind
+  int len, n, slot, tok0;
+  int r0, nq, npos;     // first position of the chunk, query tiles, positions per tile
+  int seg, segs, item;  // key segment; item: partial segments before this CTA's rows
+};
+
+__device__ __forceinline__ Work work_of(const PoolPrefillCall &c, const PoolLayerDesc &L) {
+  Work w;
+  const int u = blockIdx.x;
+  w.retr = u < c.retr_ctas;
+  const int *first = w.retr ? c.rfirst : c.sfirst;
+  const int v = w.retr ? u : u - c.retr_ctas;
+  int lo = 0, hi = c.nseq - 1;  // the last sequence with first <= v
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= v) lo = mid;
+    else hi = mid - 1;
+  }
+  w.s = lo;
+  w.len = c.len[lo];
+  w.n = c.n[lo];
+  w.slot = c.slot[lo];
+  w.tok0 = c.tok0[lo];
+  w.npos = kBM / c.G;
+  const int heads = w.retr ? c.Hr : c.Hs;
+  w.segs = w.retr ? c.segs[lo] : 1;
+  // heads fastest (neighbours in the grid read different heads' keys at the same places),
+  // then segments, then query blocks from the last -- the longest -- to the first
+  int rem = v - first[lo];
+  w.idx = rem % heads;
+  rem /= heads;
+  w.seg = rem % w.segs;
+  rem /= w.segs;
+  const int ntq = (w.n + w.npos - 1) / w.npos, blocks = (ntq + kQT - 1) / kQT, qb = blocks - 1 - rem;
+  w.g = w.retr ? L.hm.retr_head[w.idx] : L.hm.strm_head[w.idx];
+  w.r0 = qb * kQT * w.npos;
+  w.nq = min(kQT, ntq - qb * kQT);
+  w.item = c.seg0[lo] + (qb * heads + w.idx) * w.segs;
+  return w;
+}
+
+// The key tiles of a CTA as runs; returns how many runs.  Streaming heads skip tiles that
+// hold no position visible to any of the CTA's queries; the first query reaches back
+// furthest.
+//
+// Slot order: slot x < S holds position x; ring slot S + y holds the newest position
+// p = y (mod W) below len, that is, with r = len mod W, len - r + y for y < r and
+// len - r - W + y for y >= r, where it is at least S.  Query i sees it iff i - p < W.  So
+// with a = i - len + r + 1 and e = S - len + r + W the visible ring slots of i are
+//   y in [max(0, a - W, e - W), r)  and  y in [max(r, a, e), W).
+struct RingView {
+  int lo1, hi1, lo2, hi2;  // slots x (sinks included in x's origin)
+};
+__device__ __forceinline__ RingView ring_view(int i, int len, int S, int W) {
+  const int r = len % W, a = i - len + r + 1, e = S - len + r + W;
+  return {S + max(0, max(a, e) - W), S + r, S + max(r, max(a, e)), S + W};
+}
+__device__ __forceinline__ int plan_runs(const Work &w, int S, int W, Run *runs) {
+  const int rows = min(w.r0 + w.nq * w.npos, w.n);  // chunk positions 0 .. rows-1 are needed
+  const int nc = (rows + kBN - 1) / kBN;
+  int k = 0;
+  if (w.retr) {
+    if (w.len > 0) runs[k++] = {kPages, 0, (w.len + kBN - 1) / kBN};
+    runs[k++] = {kChunk, 0, nc};
+    return k;
+  }
+  int at = 0;  // tiles below are listed or skipped
+  auto add = [&](int src, int lo, int hi) {  // tiles that meet rows [lo, hi)
+    if (lo >= hi) return;
+    const int a = max(lo / kBN, at), b = (hi + kBN - 1) / kBN;
+    if (a < b) {
+      runs[k++] = {src, a, b - a};
+      at = b;
+    }
+  };
+  const RingView v = ring_view(w.len + w.r0, w.len, S, W);
+  add(kSlots, 0, min(S, w.len));
+  add(kSlots, v.lo1, v.hi1);
+  add(kSlots, v.lo2, v.hi2);
+  at = 0;
+  add(kChunk, 0, min(rows, S - w.len));
+  add(kChunk, max(0, w.r0 - W + 1), rows);
+  return k;
+}
+__device__ __forceinline__ Tile tile_at(const Run *runs, int j) {
+  while (j >= runs->count) {
+    j -= runs->count;
+    ++runs;
+  }
+  return {runs->src, (runs->first + j) * kBN};
+}
+
+// columns [lo, hi) of a 128-column tile into a 128-bit mask
+__device__ __forceinline__ void add_columns(uint32_t (&m)[4], int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int a = min(max(lo - 32 * k, 0), 32), b = min(max(hi - 32 * k, 0), 32);
+    const uint32_t below_a = a >= 32 ? ~0u : (1u << a) - 1u, below_b = b >= 32 ? ~0u : (1u << b) - 1u;
+    m[k] |= below_b & ~below_a;
+  }
+}
+
+// 128 consecutive fp32 columns of this thread's lane; one wait that names every register,
+// so that no use is scheduled before it
+#define DUO_R4(x) "+r"(r[(x)]), "+r"(r[(x) + 1]), "+r"(r[(x) + 2]), "+r"(r[(x) + 3])
+#define DUO_R16(x) DUO_R4(x), DUO_R4((x) + 4), DUO_R4((x) + 8), DUO_R4((x) + 12)
+__device__ __forceinline__ void load_row(uint32_t taddr, float (&v)[128]) {
+  uint32_t r[128];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t *q = r + 32 * c;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]),
+          "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15]), "=r"(q[16]),
+          "=r"(q[17]), "=r"(q[18]), "=r"(q[19]), "=r"(q[20]), "=r"(q[21]), "=r"(q[22]), "=r"(q[23]), "=r"(q[24]),
+          "=r"(q[25]), "=r"(q[26]), "=r"(q[27]), "=r"(q[28]), "=r"(q[29]), "=r"(q[30]), "=r"(q[31])
+        : "r"(taddr + 32 * c));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : DUO_R16(0), DUO_R16(16), DUO_R16(32), DUO_R16(48), DUO_R16(64), DUO_R16(80), DUO_R16(96), DUO_R16(112)
+               :
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+#undef DUO_R4
+#undef DUO_R16
+
+__device__ __forceinline__ float largest(const float (&v)[128]) {
+  float m[8];  // independent chains of three-input maxima
+#pragma unroll
+  for (int u = 0; u < 8; ++u) m[u] = fmaxf(v[2 * u], v[2 * u + 1]);
+#pragma unroll
+  for (int e = 16; e < 128; e += 2) {
+    float &x = m[(e >> 1) & 7];
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(x), "f"(v[e]), "f"(v[e + 1]));
+  }
+#pragma unroll
+  for (int u = 4; u > 0; u >>= 1)
+#pragma unroll
+    for (int i = 0; i < u; ++i) m[i] = fmaxf(m[i], m[i + u]);
+  return m[0];
+}
+
+// P = exp2(c v - mc) of logits v[32 B .. 32 B + 32) as bf16 pairs into columns 16 B .. of
+// `cols` (not waited for); returns their fp32 sum.  P is rounded to bf16 for the tensor
+// core (2^-9 relative, of random sign over a row); the sum takes the unrounded values.
+template <int B>
+__device__ __forceinline__ float probabilities(const float (&v)[128], float c, float mc, uint32_t cols) {
+  const uint64_t cc = pack2(c, c), mm = pack2(-mc, -mc);
+  uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+  uint32_t pk[16];
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float x0, x1;
+    unpack2(ffma2(pack2(v[32 * B + e], v[32 * B + e + 1]), cc, mm), x0, x1);
+    x0 = ex2(x0);
+    x1 = ex2(x1);
+    sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], pack2(x0, x1));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+    pk[e >> 1] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  tc::st16(cols + 16 * B, pk);
+  float a0, a1, b0, b1;
+  unpack2(sum[0], a0, a1);
+  unpack2(sum[1], b0, b1);
+  return (a0 + a1) + (b0 + b1);
+}
+
+// A V tile whose rows from `valid` on are not the sequence's: a warp copies its rows and
+// writes zeros behind them, in the layout a swizzled TMA load leaves.
+__device__ __forceinline__ void copy_ragged_tile(const char *src, int64_t row_bytes, int valid, uint32_t dst, int lane) {
+  for (int i = lane; i < kBN * 16; i += 32) {
+    const int row = i >> 4, chunk = i & 15;
+    const uint32_t to = dst + (chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    const char *from = src + (row < valid ? row : 0) * row_bytes + chunk * 16;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(row < valid ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  tc::fence_async_smem();
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_constant__ PoolPrefillCall c) {
+  extern __shared__ char smem_raw[];
+  char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + kSmBar + 8u * i; };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kSmMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSmMisc + 4);
+  int *span = reinterpret_cast<int *>(smem + kSmMisc + 8);  // tiles [span[0], span[1]) of the runs
+  Run *runs = reinterpret_cast<Run *>(smem + kSmMisc + 16);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PoolLayerDesc &L = *c.layer;
+  const Work w = work_of(c, L);
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i >= kBarPFull && i < kBarPFull + kQT) ? kBM / 32 : 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+    const int k = plan_runs(w, c.S, c.W, runs);
+    int total = 0;
+    for (int i = 0; i < k; ++i) total += runs[i].count;
+    span[0] = static_cast<int>(static_cast<int64_t>(total) * w.seg / w.segs);
+    span[1] = static_cast<int>(static_cast<int64_t>(total) * (w.seg + 1) / w.segs);
+  }
+  if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int j0 = span[0], nt = span[1] - span[0];
+
+  if (warp == 0 || warp == 2) {
+    // ================= producers: warp 0 Q and K, warp 2 V =================
+    const bool is_k = warp == 0;
+    const CUtensorMap *pages = is_k ? &L.tm_kr : &L.tm_vr, *slots = is_k ? &L.tm_ks : &L.tm_vs;
+    const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
+    if (lane == 0) {
+      // the layer's maps live in device memory, written before this launch
+      const CUtensorMap *m = w.retr ? pages : slots;
+      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+      if (is_k) {
+        mbar_expect_tx(bar(kBarQ), 256 * c.G * w.npos * w.nq);
+        for (int t = 0; t < w.nq; ++t)
+          for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
+            tc::tma_3d(sbase + kSmQ + t * kTile + h * kHalf, &c.tm_q, 64 * h, w.g * c.G, w.tok0 + w.r0 + t * w.npos,
+                       bar(kBarQ));
+      }
+    }
+    const int *row = c.table + static_cast<int64_t>(w.slot) * c.pages_per_seq;
+    const uint32_t stage0 = sbase + (is_k ? kSmK : kSmV);
+    const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
+    constexpr int kStages = kKStages;
+    static_assert(kKStages == kVStages, "one producer loop for both rings");
+    int issued = 0;
+    Tile t = nt > 0 ? tile_at(runs, j0) : Tile{kChunk, 0};
+    int page = t.src == kPages ? row[t.y / kBN] : 0;
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % kStages;
+      // the next tile's page number is on its way while this one waits for its stage
+      Tile next = t;
+      int next_page = 0;
+      if (j + 1 < nt) {
+        next = tile_at(runs, j0 + j + 1);
+        if (next.src == kPages) next_page = row[next.y / kBN];
+      }
+      bool ok = true;
+      if (lane == 0 && j >= kStages)
+        ok = tc::wait_bar(bar(empty0 + s), ((j / kStages) - 1) & 1, c.status, abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      __syncwarp();
+      const uint32_t dst = stage0 + s * kTile, fb = bar(full0 + s);
+      const int valid = t.src == kChunk ? w.n - t.y : kBN;
+      if (!is_k && valid < kBN) {
+        copy_ragged_tile(c.v + (static_cast<int64_t>(w.tok0 + t.y) * c.Hkv + w.g) * 256,
+                         static_cast<int64_t>(c.Hkv) * 256, valid, dst, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fb);
+      } else if (lane == 0) {
+        mbar_expect_tx(fb, kTile);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t to = dst + h * kHalf;
+          if (t.src == kPages) tc::tma_3d(to, pages, 64 * h, 0, page * c.Hr + w.idx, fb);
+          else if (t.src == kSlots) tc::tma_3d(to, slots, 64 * h, t.y, w.slot * c.Hs + w.idx, fb);
+          else tc::tma_3d(to, chunk, 64 * h, w.g, w.tok0 + t.y, fb);
+        }
+      }
+      ++issued;
+      t = next;
+      page = next_page;
+    }
+    if (lane == 0) {  // nothing may still be landing in shared memory when the CTA ends
+      if (is_k) mbar_wait(bar(kBarQ), 0, c.status);
+      tc::drain_loads(bar(full0), kStages, issued, c.status);
+    }
+  } else if (warp == 1) {
+    // ================= MMA issuer =================
+    if (lane == 0) {
+      constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, false, false);
+      constexpr uint32_t kIdPV = tc::idesc_bf16(kBM, kD, false, true);
+      // operands lie below 256 KiB, so one at byte offset o is the base's descriptor + (o >> 4)
+      const uint64_t qd0 = tc::sdesc(sbase + kSmQ, 16, 1024), kd0 = tc::sdesc(sbase + kSmK, 16, 1024);
+      const uint64_t vd0 = tc::sdesc(sbase + kSmV, kHalf, 1024);
+      // S_t(j) = Q_t K_j^T, d 128 in 8 steps of 16
+      auto issue_s = [&](int t, int j) {
+        const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + (j % kKStages) * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          tc::mma_ss(tmem + kTmS + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
+        }
+        tc::commit(bar(kBarSFull + t));
+      };
+      // O_t += P_t(j) V_j, 128 keys in 8 steps of 16
+      auto issue_pv = [&](int t, int j) {
+        const uint64_t vd = vd0 + (j % kVStages) * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ts(tmem + kTmO + t * 128, tmem + kTmS + t * 128 + kk * 8, vd + kk * (2048 >> 4), kIdPV,
+                     kk > 0 || j > 0 ? 1u : 0u);
+      };
+      bool ok = nt > 0 && tc::wait_bar(bar(kBarQ), 0, c.status, abort_flag) &&
+                tc::wait_bar(bar(kBarKFull), 0, c.status, abort_flag);
+      if (ok) {
+        tc::fence_after();
+        for (int t = 0; t < w.nq; ++t) issue_s(t, 0);
+        tc::commit(bar(kBarKEmpty));
+      }
+      for (int j = 0; j < nt && ok; ++j) {
+        for (int t = 0; t < w.nq && ok; ++t) {
+          ok = tc::wait_bar(bar(kBarPFull + t), j & 1, c.status, abort_flag);
+          if (ok && t == 0)
+            ok = tc::wait_bar(bar(kBarVFull + (j % kVStages)), (j / kVStages) & 1, c.status, abort_flag);
+          if (!ok) break;
+          tc::fence_after();
+          issue_pv(t, j);
+          if (t == w.nq - 1) tc::commit(bar(kBarVEmpty + (j % kVStages)));
+          if (j + 1 == nt) {
+            tc::commit(bar(kBarOFull + t));
+            continue;
+          }
+          if (t == 0) {
+            ok = tc::wait_bar(bar(kBarKFull + ((j + 1) % kKStages)), ((j + 1) / kKStages) & 1, c.status, abort_flag);
+            if (!ok) break;
+            tc::fence_after();
+          }
+          issue_s(t, j + 1);
+          if (t == w.nq - 1) tc::commit(bar(kBarKEmpty + ((j + 1) % kKStages)));
+        }
+      }
+      // every MMA issued has completed before TMEM is freed
+      tc::commit(bar(kBarDrain));
+      mbar_wait(bar(kBarDrain), 0, c.status);
+    }
+  } else if (warp >= kSoftWarp0 && (warp - kSoftWarp0) / 4 < w.nq) {
+    // ================= softmax of query tile qt: one thread per query row =================
+    constexpr float kSlack = 8.0f;
+    const int qt = (warp - kSoftWarp0) >> 2, row = ((warp & 3) << 5) | lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) << 5) << 16);
+    const uint32_t s_cols = lane_base + kTmS + qt * 128, o_cols = lane_base + kTmO + qt * 128;
+    const int rpos = w.r0 + qt * w.npos + row / c.G;  // position of the row in the chunk
+    const int i = w.len + rpos;                       // and in the sequence
+    const float scale = c.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+
+    for (int j = 0; j < nt; ++j) {
+      // columns of the tile that this row sees; most tiles are seen whole
+      const Tile t = tile_at(runs, j0 + j);
+      const int base = w.len + t.y, end = min(i - base + 1, w.n - t.y);  // of a chunk tile
+      const bool whole = t.src == kPages   ? t.y + kBN <= w.len
+                         : t.src == kChunk ? end >= kBN && (w.retr || base + kBN <= c.S || i - c.W < base)
+                                           : false;
+      uint32_t vis[4] = {0u, 0u, 0u, 0u};
+      if (!whole) {
+        if (t.src == kPages) {
+          add_columns(vis, 0, w.len - t.y);
+        } else if (t.src == kSlots) {
+          const RingView v = ring_view(i, w.len, c.S, c.W);
+          add_columns(vis, 0, min(c.S, w.len) - t.y);
+          add_columns(vis, v.lo1 - t.y, v.hi1 - t.y);
+          add_columns(vis, v.lo2 - t.y, v.hi2 - t.y);
+        } else if (w.retr) {
+          add_columns(vis, 0, end);
+        } else {
+          add_columns(vis, 0, min(end, c.S - base));
+          add_columns(vis, i - c.W + 1 - base, end);
+        }
+      }
+
+      if (ok) ok = tc::wait_bar(bar(kBarSFull + qt), j & 1, c.status, abort_flag);
+      tc::fence_after();
+      float v[128];
+      load_row(s_cols, v);
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e) v[e] = (vis[e >> 5] >> (e & 31)) & 1u ? v[e] : -INFINITY;
+      }
+      const float tmax = largest(v) * scale;  // -inf when the row sees nothing of the tile
+      const bool need = tmax > m + kSlack;
+      float alpha = 1.f;
+      if (need) {
+        alpha = ex2(m - tmax);  // 0 while m is -inf
+        m = tmax;
+      }
+      if (j >= 1 && __any_sync(0xffffffffu, need)) {
+        // S_t(j) has landed, so P_t(j-1) V_{j-1} has too: rescale O_t in place
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          float x[16];
+          tc::ld<16>(o_cols + 16 * q, x);
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * alpha);
+          tc::st16(o_cols + 16 * q, u);
+        }
+        tc::st_wait();
+      }
+      const float mc = m == -INFINITY ? 0.f : m;  // masked logits are -inf and give 0
+      float sum = probabilities<0>(v, scale, mc, s_cols) + probabilities<1>(v, scale, mc, s_cols);
+      sum += probabilities<2>(v, scale, mc, s_cols) + probabilities<3>(v, scale, mc, s_cols);
+      tc::st_wait();
+      tc::fence_before();
+      mbar_arrive_warp(bar(kBarPFull + qt));
+      l = fmaf(l, alpha, sum);
+    }
+    if (nt > 0 && ok) ok = tc::wait_bar(bar(kBarOFull + qt), 0, c.status, abort_flag);
+    tc::fence_after();
+    const bool live = row < c.G * w.npos && rpos < w.n;
+    if (w.segs > 1) {
+      // a segment's row as it is; it may have seen nothing (m = -inf, l = 0)
+      float *part = c.partials + (static_cast<int64_t>(w.item + w.seg) * kPrefillRows + qt * kBM + row) * kPrefillRow;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float x[32];
+        tc::ld<32>(o_cols + 32 * q, x);
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(part + 32 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        }
+      }
+      if (live) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
+    } else {
+      const int64_t at = static_cast<int64_t>(w.tok0 + rpos) * c.Hq + w.g * c.G + row % c.G;
+      const float inv = 1.f / l;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        float x[32];
+        tc::ld<32>(o_cols + 32 * q, x);
+        if (live) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * u + 2 * e] * inv, x[8 * u + 2 * e + 1] * inv);
+              p[e] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            *reinterpret_cast<uint4 *>(c.out + at * (kD * 2) + q * 64 + u * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+        }
+      }
+      if (live && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 1) tc::tmem_free(tmem, 512);
+}
+
+}  // namespace
+
+// Every host step that can fail: tensor maps, the shared-memory limit.
+cudaError_t prepare_prefill_pool_tc(PoolPrefillCall *c, const void *q, const void *k, const void *v, int tokens) {
+  const uint64_t row = kD * 2, T = static_cast<uint64_t>(tokens);
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t dq[3] = {kD, static_cast<uint64_t>(c->Hq), T}, sq[2] = {row, row * c->Hq};
+  const uint32_t bq[3] = {64, static_cast<uint32_t>(c->G), static_cast<uint32_t>(kBM / c->G)};
+  const uint64_t dk[3] = {kD, static_cast<uint64_t>(c->Hkv), T}, sk[2] = {row, row * c->Hkv};
+  const uint32_t bk[3] = {64, 1, kBN};
+  if (!tc::make_map(&c->tm_q, bf, q, 3, dq, sq, bq, sw) || !tc::make_map(&c->tm_k, bf, k, 3, dk, sk, bk, sw) ||
+      !tc::make_map(&c->tm_v, bf, v, 3, dk, sk, bk, sw))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> attr{0};
+  return opt_in_smem(prefill_pool_kernel, kSmemAlloc, attr);
+}
+
+cudaError_t launch_prefill_pool_tc(const PoolPrefillCall &c, cudaStream_t st) {
+  prefill_pool_kernel<<<c.ctas, kThreads, kSmemAlloc, st>>>(c);
+  return cudaGetLastError();
+}
+
+}  // namespace duo

@@ -52,4 +52,40 @@ namespace duo {
 // First use of a pool: clears its buffer and describes its layers on the device.
 duo_status pool_init(duo_pool *P, cudaStream_t st);
 
+// ---- pre-fill attention over a pool ----
+constexpr int kPrefillMaxTokens = 1 << 18;  // tokens of one call
+// pages that a call's tokens can touch: theirs, and a partial one at either end of each
+constexpr int kPrefillMaxPages = kPrefillMaxTokens / kPoolTile + 2 * kPoolMaxSeqs;
+constexpr int kPrefillRows = 256;           // query rows of a CTA (two tensor-core tiles)
+constexpr int kPrefillSegs = 160;           // key segments whose partial rows fit the scratch
+constexpr int kPrefillRow = 132;            // floats of a partial row: 128 sums, max, sum of weights, 2 unused
+
+// The attention launch.  Sequences are listed by decreasing work per CTA; CTAs of
+// retrieval heads come first.
+struct PoolPrefillCall {
+  CUtensorMap tm_q, tm_k, tm_v;  // q [tokens][Hq][d], k and v [tokens][Hkv][d]
+  const PoolLayerDesc *layer;    // device
+  const int *table;              // device block table [max_seqs][pages_per_seq]
+  int pages_per_seq;
+  const char *v;
+  char *out;
+  float *lse, *partials;
+  uint32_t *status;
+  int nseq, Hq, Hkv, G, S, W, Hr, Hs, retr_ctas, ctas;
+  float scale_log2;
+  int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
+  int tok0[kPoolMaxSeqs];        // first of the sequence's tokens in the call's tensors
+  int segs[kPoolMaxSeqs];        // key segments of each of its retrieval CTAs' rows
+  int seg0[kPoolMaxSeqs];        // its first partial segment (segs > 1)
+  int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // CTAs before a sequence, per kind
+};
+// Positions per query tile and CTAs (of two tiles) that cover n positions of one KV head.
+inline int prefill_tile_positions(int G) { return 128 / G; }
+inline int prefill_blocks(int n, int G) {
+  const int per = 2 * prefill_tile_positions(G);
+  return (n + per - 1) / per;
+}
+cudaError_t prepare_prefill_pool_tc(PoolPrefillCall *c, const void *q, const void *k, const void *v, int tokens);
+cudaError_t launch_prefill_pool_tc(const PoolPrefillCall &c, cudaStream_t st);
+
 }  // namespace duo

@@ -102,6 +102,9 @@ def lib() -> ctypes.CDLL:
             L.duo_pool_append_kv.argtypes = [vp, i32, i32, vp, vp, i32, vp]
             L.duo_pool_decode_step.restype = i32
             L.duo_pool_decode_step.argtypes = [vp, i32, i32, i32, ctypes.POINTER(i32), vp, vp, vp, vp, vp, vp]
+            L.duo_pool_prefill.restype = i32
+            L.duo_pool_prefill.argtypes = [vp, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32), vp, vp, vp, vp, vp,
+                                           vp]
             L.duo_pool_fork.restype = i32
             L.duo_pool_fork.argtypes = [vp, i32, i32, vp, ctypes.POINTER(i32)]
             L.duo_pool_copy.restype = i32
@@ -281,6 +284,13 @@ def duo_pool_decode_step(handle, layer0, nlayers, seqs, q, k, v, out, lse, strea
     arr = (ctypes.c_int * len(seqs))(*[int(x) for x in seqs])
     return lib().duo_pool_decode_step(handle, layer0, nlayers, len(seqs), arr, _ptr(q), _ptr(k), _ptr(v), _ptr(out),
                                       _ptr(lse), _ptr(stream))
+
+
+def duo_pool_prefill(handle, layer, seqs, n, q, k, v, out, lse, stream=None) -> int:
+    m = len(seqs)
+    ints = ctypes.c_int * m
+    return lib().duo_pool_prefill(handle, layer, m, ints(*seqs), ints(*n), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                  _ptr(lse), _ptr(stream))
 
 
 def duo_pool_fork(handle, seq, n, stream=None):
@@ -543,6 +553,29 @@ class DuoPool:
             lse = torch.empty(nlayers, ns, self.q_heads, dtype=torch.float32, device=q.device)
         self._check(duo_pool_decode_step(self.handle, layer0, nlayers, seqs, q, k, v, out, lse, _stream_ptr(stream)),
                     "duo_pool_decode_step")
+        return out, lse
+
+    def prefill(self, layer, seqs, n, q, k, v, out=None, lse=None, want_lse=True, stream=None):
+        """duo_pool_prefill: the n[i] tokens of each listed sequence attend and are appended; q, out
+        [sum n][Hq][128], k, v [sum n][Hkv][128] bf16, sequence after sequence -> (out, lse)."""
+        if len(n) != len(seqs):
+            raise ValueError(f"n: expected {len(seqs)} lengths, got {len(n)}")
+        tokens, dev = sum(n), self.buffer.device
+        shapes = (tokens, self.q_heads, 128), (tokens, self.kv_heads, 128)
+        for t, name, shape in ((q, "q", shapes[0]), (k, "k", shapes[1]), (v, "v", shapes[1]), (out, "out", shapes[0])):
+            if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape or not t.is_contiguous() or
+                                  t.device != dev):
+                raise ValueError(f"{name}: expected contiguous bf16 {list(shape)} on {dev}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty(shapes[0][:2], dtype=torch.float32, device=dev)
+        elif lse is not None and (lse.dtype != torch.float32 or lse.shape != shapes[0][:2] or
+                                  not lse.is_contiguous() or lse.device != dev):
+            raise ValueError(f"lse: expected contiguous fp32 {list(shapes[0][:2])} on {dev}")
+        self._check(duo_pool_prefill(self.handle, layer, seqs, n, q, k, v, out, lse, self._stream(stream)),
+                    "duo_pool_prefill")
         return out, lse
 
     def fork(self, seq, n=1, stream=None):

@@ -316,6 +316,26 @@ DUO_API duo_status duo_pool_append_kv(duo_pool *pool, int layer, int seq, const 
                                       void *cuda_stream);
 
 /*
+ * Pre-fill attention of a ragged batch on one layer: for each of the nseq listed sequences
+ * (host array `seqs`, distinct, open) the n[i] >= 1 tokens at positions len .. len+n[i]-1
+ * attend to the sequence's cached tokens and to one another -- causal mask for retrieval
+ * heads, Lambda mask for streaming heads, as duo_prefill_chunk does for a cache -- and are
+ * then appended as by duo_pool_append_kv.  Any mix of first prompts, continued chunks,
+ * drafts to be checked and single tokens; sequences of a fork read their shared pages.
+ *   q, out  device [tokens][Hq][d];  k, v  device [tokens][Hkv][d], the tokens of seqs[0],
+ *           then those of seqs[1], ... (tokens = sum of n[i]);  lse [tokens][Hq] fp32, or NULL
+ * A sequence's results do not depend on the other sequences' values.  Within a sequence k
+ * and v must be finite: a row that is not spoils queries that do not see it too.
+ * Two launches: the attention, which reads pages, sinks, rings, k and v where they are (the
+ * keys of few queries over a long history are split over CTAs, with partial rows in the
+ * pool's scratch), then one that joins split rows and appends.  nseq <= 128, at most
+ * 262144 tokens (else DUO_ERR_INVALID).  DUO_ERR_CAPACITY past max_len or without free
+ * pages; on any error the cache is unchanged.
+ */
+DUO_API duo_status duo_pool_prefill(duo_pool *pool, int layer, int nseq, const int *seqs, const int *n, const void *q,
+                                    const void *k, const void *v, void *out, float *lse, void *cuda_stream);
+
+/*
  * One decode step of a ragged batch: for each of the nseq listed sequences (host array
  * `seqs`, distinct, open) and each layer layer0 .. layer0+nlayers-1, append the token
  * (k, v [nlayers][nseq][Hkv][d]) at the sequence's length, then attend with its query
