@@ -11,24 +11,27 @@
 // (the softmax does not ask for an order; masks say which slot holds a visible position),
 // and the call's own k and v.  The cache is only read; the append is a later launch.
 //
-// One CTA = two 128-row query tiles of one (sequence, KV head) -- a row is one of G query
+// An item is two 128-row query tiles of one (sequence, KV head) -- a row is one of G query
 // heads at one of 128 / G consecutive positions (rows past G * (128 / G) idle) -- sharing
-// every K/V tile; 12 warps:
+// every K/V tile.  The grid is one CTA per SM; a CTA works through whole items and then
+// through its share of the last ones, which are cut by key tiles so that every CTA gets
+// the same number of them (few queries over a long history are nothing but that share).
+// A cut item's CTAs leave unnormalised rows, max and sum in the scratch; the append launch
+// that follows joins them.  12 warps:
 //   warp 0      TMA: both Q tiles, then the K ring (2 stages)
 //   warp 1      owns TMEM; lane 0 issues every tcgen05.mma
 //   warp 2      the V ring (2 stages); by TMA, but the last tile of a chunk row by row:
 //               rows behind it belong to the next sequence, and 0 * NaN would carry a
 //               broken neighbour's values over, so they are written as zeros
+//   warp 3      lists the CTA's pieces for the others, up to four ahead
 //   warps 4-7 and 8-11  softmax of query tile 0 and 1, one thread per row
 // TMEM: S_t at 128 t (P_t, bf16 pairs, over its first 64 columns), O_t at 256 + 128 t.
 // The MMA thread issues PV_0(j), S_0(j+1), PV_1(j), S_1(j+1): one tile's products run
 // while the other tile's softmax works.  MMAs of one thread complete in order, so S_t(j+1)
 // overwrites P_t(j) after PV_t(j) has read it, and once S_t(j) has landed O_t may be
-// rescaled in place.
-//
-// Few rows over a long history would leave most SMs idle: then a CTA's keys are split
-// into segments, each a CTA that leaves unnormalised rows, max and sum in the scratch; the
-// append launch that follows joins them.
+// rescaled in place.  The next piece's first products overwrite S_t after the last
+// PV_t has read P_t, and O_t after its softmax warps, which have read it out, have
+// published their next P_t.
 //
 // Every mbarrier wait is bounded; one that runs out latches kDevTimeout, and every role
 // drains and exits.
@@ -48,111 +51,60 @@ constexpr int kHalf = 16384;
 
 constexpr int kSmQ = 0, kSmK = kSmQ + kQT * kTile, kSmV = kSmK + kKStages * kTile, kSmBar = kSmV + kVStages * kTile;
 constexpr int kSmMisc = kSmBar + 256;
-constexpr int kSmemAlloc = kSmMisc + 256 + 1024;  // slack for aligning the base to 1 KiB
+constexpr int kPieces = 4;  // pieces listed ahead
+constexpr int kSmemAlloc = kSmMisc + 768 + 1024;  // slack for aligning the base to 1 KiB
 constexpr int kTmS = 0, kTmO = 256;
+constexpr int kPFirst = 96;  // keys of a tile whose P is handed over first
 
-constexpr int kBarQ = 0, kBarKFull = 1, kBarKEmpty = kBarKFull + kKStages, kBarVFull = kBarKEmpty + kKStages,
+constexpr int kBarQ = 0, kBarQEmpty = 1, kBarKFull = 2, kBarKEmpty = kBarKFull + kKStages, kBarVFull = kBarKEmpty + kKStages,
               kBarVEmpty = kBarVFull + kVStages, kBarSFull = kBarVEmpty + kVStages, kBarPFull = kBarSFull + kQT,
-              kBarOFull = kBarPFull + kQT, kBarDrain = kBarOFull + kQT, kNumBars = kBarDrain + 1;
+              kBarPRest = kBarPFull + kQT, kBarOFull = kBarPRest + kQT, kBarPiece = kBarOFull + kQT, kBarPieceFree = kBarPiece + kPieces,
+              kBarDrain = kBarPieceFree + kPieces, kNumBars = kBarDrain + 1;
 static_assert(kNumBars * 8 <= 256 && kSmemAlloc <= 227 * 1024, "shared memory");
 
-enum Source { kPages, kSlots, kChunk };
-
-// A run of consecutive key tiles of one source.
-struct Run {
-  int src, first, count;
+// A piece of a CTA's work: key tiles [j0, j0 + nt) of an item.
+struct Piece {
+  int g, idx, retr;     // KV head, its index among heads of its kind
+  int len, n, slot, tok0;
+  int r0, nq;           // first position in the chunk, query tiles
+  int j0, nt;           // nt = 0: the CTA's work is done
+  int part;             // partial rows' place in the scratch, -1: the whole item
+  PrefillRun runs[kPrefillMaxRuns];
 };
+static_assert(sizeof(Piece) * kPieces + 16 <= 768, "shared memory");
 struct Tile {
   int src, y;  // source, first row
 };
 
-// What a CTA works on, the same in every thread.
-struct Work {
-  int s, g, idx, retr;  // listed sequence, KV head, its index among heads of its kind
-  int len, n, slot, tok0;
-  int r0, nq, npos;     // first position of the chunk, query tiles, positions per tile
-  int seg, segs, item;  // key segment; item: partial segments before this CTA's rows
-};
-
-__device__ __forceinline__ Work work_of(const PoolPrefillCall &c, const PoolLayerDesc &L) {
-  Work w;
-  const int u = blockIdx.x;
-  w.retr = u < c.retr_ctas;
+// Item `u` of the call; its tiles go into `runs`.  Returns how many there are.
+__device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PoolLayerDesc &L, int u, Piece &w) {
+  w.retr = u < c.retr_items;
   const int *first = w.retr ? c.rfirst : c.sfirst;
-  const int v = w.retr ? u : u - c.retr_ctas;
+  const int v = w.retr ? u : u - c.retr_items;
   int lo = 0, hi = c.nseq - 1;  // the last sequence with first <= v
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (first[mid] <= v) lo = mid;
     else hi = mid - 1;
   }
-  w.s = lo;
   w.len = c.len[lo];
   w.n = c.n[lo];
   w.slot = c.slot[lo];
   w.tok0 = c.tok0[lo];
-  w.npos = kBM / c.G;
-  const int heads = w.retr ? c.Hr : c.Hs;
-  w.segs = w.retr ? c.segs[lo] : 1;
   // heads fastest (neighbours in the grid read different heads' keys at the same places),
-  // then segments, then query blocks from the last -- the longest -- to the first
-  int rem = v - first[lo];
+  // query blocks from the last -- the longest -- to the first
+  const int npos = kBM / c.G, heads = w.retr ? c.Hr : c.Hs, rem = v - first[lo];
+  const int ntq = (w.n + npos - 1) / npos, blocks = (ntq + kQT - 1) / kQT, qb = blocks - 1 - rem / heads;
   w.idx = rem % heads;
-  rem /= heads;
-  w.seg = rem % w.segs;
-  rem /= w.segs;
-  const int ntq = (w.n + w.npos - 1) / w.npos, blocks = (ntq + kQT - 1) / kQT, qb = blocks - 1 - rem;
   w.g = w.retr ? L.hm.retr_head[w.idx] : L.hm.strm_head[w.idx];
-  w.r0 = qb * kQT * w.npos;
+  w.r0 = qb * kQT * npos;
   w.nq = min(kQT, ntq - qb * kQT);
-  w.item = c.seg0[lo] + (qb * heads + w.idx) * w.segs;
-  return w;
+  const int k = prefill_runs(w.retr, w.len, w.n, w.r0, npos, c.S, c.W, w.runs);
+  int tiles = 0;
+  for (int i = 0; i < k; ++i) tiles += w.runs[i].count;
+  return tiles;
 }
-
-// The key tiles of a CTA as runs; returns how many runs.  Streaming heads skip tiles that
-// hold no position visible to any of the CTA's queries; the first query reaches back
-// furthest.
-//
-// Slot order: slot x < S holds position x; ring slot S + y holds the newest position
-// p = y (mod W) below len, that is, with r = len mod W, len - r + y for y < r and
-// len - r - W + y for y >= r, where it is at least S.  Query i sees it iff i - p < W.  So
-// with a = i - len + r + 1 and e = S - len + r + W the visible ring slots of i are
-//   y in [max(0, a - W, e - W), r)  and  y in [max(r, a, e), W).
-struct RingView {
-  int lo1, hi1, lo2, hi2;  // slots x (sinks included in x's origin)
-};
-__device__ __forceinline__ RingView ring_view(int i, int len, int S, int W) {
-  const int r = len % W, a = i - len + r + 1, e = S - len + r + W;
-  return {S + max(0, max(a, e) - W), S + r, S + max(r, max(a, e)), S + W};
-}
-__device__ __forceinline__ int plan_runs(const Work &w, int S, int W, Run *runs) {
-  const int rows = min(w.r0 + w.nq * w.npos, w.n);  // chunk positions 0 .. rows-1 are needed
-  const int nc = (rows + kBN - 1) / kBN;
-  int k = 0;
-  if (w.retr) {
-    if (w.len > 0) runs[k++] = {kPages, 0, (w.len + kBN - 1) / kBN};
-    runs[k++] = {kChunk, 0, nc};
-    return k;
-  }
-  int at = 0;  // tiles below are listed or skipped
-  auto add = [&](int src, int lo, int hi) {  // tiles that meet rows [lo, hi)
-    if (lo >= hi) return;
-    const int a = max(lo / kBN, at), b = (hi + kBN - 1) / kBN;
-    if (a < b) {
-      runs[k++] = {src, a, b - a};
-      at = b;
-    }
-  };
-  const RingView v = ring_view(w.len + w.r0, w.len, S, W);
-  add(kSlots, 0, min(S, w.len));
-  add(kSlots, v.lo1, v.hi1);
-  add(kSlots, v.lo2, v.hi2);
-  at = 0;
-  add(kChunk, 0, min(rows, S - w.len));
-  add(kChunk, max(0, w.r0 - W + 1), rows);
-  return k;
-}
-__device__ __forceinline__ Tile tile_at(const Run *runs, int j) {
+__device__ __forceinline__ Tile tile_at(const PrefillRun *runs, int j) {
   while (j >= runs->count) {
     j -= runs->count;
     ++runs;
@@ -261,262 +213,402 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
   auto bar = [&](int i) { return sbase + kSmBar + 8u * i; };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kSmMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSmMisc + 4);
-  int *span = reinterpret_cast<int *>(smem + kSmMisc + 8);  // tiles [span[0], span[1]) of the runs
-  Run *runs = reinterpret_cast<Run *>(smem + kSmMisc + 16);
+  Piece *pieces = reinterpret_cast<Piece *>(smem + kSmMisc + 16);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PoolLayerDesc &L = *c.layer;
-  const Work w = work_of(c, L);
+  const int npos = kBM / c.G;  // positions of a query tile
 
   if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i >= kBarPFull && i < kBarPFull + kQT) ? kBM / 32 : 1);
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool softmax = i >= kBarPFull && i < kBarPFull + 2 * kQT, listed = i >= kBarPieceFree && i < kBarPieceFree + kPieces;
+      mbar_init(bar(i), softmax ? kBM / 32 : listed ? 3 + 4 * kQT : 1);
+    }
     fence_mbar_init();
     *abort_flag = 0;
-    const int k = plan_runs(w, c.S, c.W, runs);
-    int total = 0;
-    for (int i = 0; i < k; ++i) total += runs[i].count;
-    span[0] = static_cast<int>(static_cast<int64_t>(total) * w.seg / w.segs);
-    span[1] = static_cast<int>(static_cast<int64_t>(total) * (w.seg + 1) / w.segs);
   }
   if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int j0 = span[0], nt = span[1] - span[0];
 
-  if (warp == 0 || warp == 2) {
-    // ================= producers: warp 0 Q and K, warp 2 V =================
-    const bool is_k = warp == 0;
-    const CUtensorMap *pages = is_k ? &L.tm_kr : &L.tm_vr, *slots = is_k ? &L.tm_ks : &L.tm_vs;
-    const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
+  // The roles take the pieces in order: piece p is at p % kPieces while they hold it.
+  auto take = [&](int p, bool &ok) -> const Piece * {
+    if (ok) ok = tc::wait_bar(bar(kBarPiece + p % kPieces), (p / kPieces) & 1, c.status, abort_flag);
+    return ok ? pieces + p % kPieces : nullptr;
+  };
+  auto leave = [&](int p) { mbar_arrive(bar(kBarPieceFree + p % kPieces)); };
+
+  // Shares of the launch's 384 * 168 registers: the softmax warps hold a row of logits.
+  if (warp < kSoftWarp0) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == 3) {
+    // ================= lists the pieces =================
     if (lane == 0) {
-      // the layer's maps live in device memory, written before this launch
-      const CUtensorMap *m = w.retr ? pages : slots;
-      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
-      if (is_k) {
-        mbar_expect_tx(bar(kBarQ), 256 * c.G * w.npos * w.nq);
-        for (int t = 0; t < w.nq; ++t)
-          for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
-            tc::tma_3d(sbase + kSmQ + t * kTile + h * kHalf, &c.tm_q, 64 * h, w.g * c.G, w.tok0 + w.r0 + t * w.npos,
-                       bar(kBarQ));
+      int p = 0;
+      bool ok = true;
+      auto slot = [&]() -> Piece * {
+        if (p >= kPieces)
+          ok = tc::wait_bar(bar(kBarPieceFree + p % kPieces), (p / kPieces - 1) & 1, c.status, abort_flag);
+        return ok ? pieces + p % kPieces : nullptr;
+      };
+      auto publish = [&] {
+        mbar_arrive(bar(kBarPiece + p % kPieces));
+        ++p;
+      };
+      for (int u = blockIdx.x; u < c.whole_items; u += gridDim.x) {
+        Piece *w = slot();
+        if (!ok) break;
+        w->nt = item_of(c, L, u, *w);
+        w->j0 = 0;
+        w->part = -1;
+        publish();
+      }
+      const PrefillShare sh = c.share[blockIdx.x];
+      int j0 = sh.tile, left = sh.tiles;
+      for (int u = sh.item; left > 0 && ok; ++u) {
+        Piece *w = slot();
+        if (!ok) break;
+        const int tiles = item_of(c, L, u, *w), nt = min(tiles - j0, left);
+        w->j0 = j0;
+        w->nt = nt;
+        w->part = nt == tiles ? -1 : (u == sh.item ? sh.part : sh.part + 1);
+        left -= nt;
+        j0 = 0;
+        publish();
+      }
+      if (ok) {
+        Piece *w = slot();
+        if (ok) {
+          w->nt = 0;
+          publish();
+        }
       }
     }
-    const int *row = c.table + static_cast<int64_t>(w.slot) * c.pages_per_seq;
+  } else if (warp == 0 || warp == 2) {
+    // ================= producers: warp 0 Q and K, warp 2 V =================
+    const bool is_k = warp == 0;
+    if (lane == 0) {
+      // the layer's maps live in device memory, written before this launch
+      const CUtensorMap *m = is_k ? &L.tm_kr : &L.tm_vr;
+      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+      m = is_k ? &L.tm_ks : &L.tm_vs;
+      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+    }
     const uint32_t stage0 = sbase + (is_k ? kSmK : kSmV);
     const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
     constexpr int kStages = kKStages;
     static_assert(kKStages == kVStages, "one producer loop for both rings");
-    int issued = 0;
-    Tile t = nt > 0 ? tile_at(runs, j0) : Tile{kChunk, 0};
-    int page = t.src == kPages ? row[t.y / kBN] : 0;
-    for (int j = 0; j < nt; ++j) {
-      const int s = j % kStages;
-      // the next tile's page number is on its way while this one waits for its stage
-      Tile next = t;
-      int next_page = 0;
-      if (j + 1 < nt) {
-        next = tile_at(runs, j0 + j + 1);
-        if (next.src == kPages) next_page = row[next.y / kBN];
-      }
-      bool ok = true;
-      if (lane == 0 && j >= kStages)
-        ok = tc::wait_bar(bar(empty0 + s), ((j / kStages) - 1) & 1, c.status, abort_flag);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      __syncwarp();
-      const uint32_t dst = stage0 + s * kTile, fb = bar(full0 + s);
-      const int valid = t.src == kChunk ? w.n - t.y : kBN;
-      if (!is_k && valid < kBN) {
-        copy_ragged_tile(c.v + (static_cast<int64_t>(w.tok0 + t.y) * c.Hkv + w.g) * 256,
-                         static_cast<int64_t>(c.Hkv) * 256, valid, dst, lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(fb);
-      } else if (lane == 0) {
-        mbar_expect_tx(fb, kTile);
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t to = dst + h * kHalf;
-          if (t.src == kPages) tc::tma_3d(to, pages, 64 * h, 0, page * c.Hr + w.idx, fb);
-          else if (t.src == kSlots) tc::tma_3d(to, slots, 64 * h, t.y, w.slot * c.Hs + w.idx, fb);
-          else tc::tma_3d(to, chunk, 64 * h, w.g, w.tok0 + t.y, fb);
+    int issued = 0, queries = 0;
+    bool ok = true;
+    for (int p = 0;; ++p) {
+      const Piece *w = take(p, ok);
+      if (!__all_sync(0xffffffffu, ok) || w->nt == 0) break;
+      if (is_k) {
+        if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
+        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
+          for (int t = 0; t < w->nq; ++t)
+            for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
+              tc::tma_3d(sbase + kSmQ + t * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G, w->tok0 + w->r0 + t * npos,
+                         bar(kBarQ));
         }
+        ++queries;
       }
-      ++issued;
-      t = next;
-      page = next_page;
+      const CUtensorMap *pages = is_k ? &L.tm_kr : &L.tm_vr, *slots = is_k ? &L.tm_ks : &L.tm_vs;
+      const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
+      const int *row = c.table + static_cast<int64_t>(w->slot) * c.pages_per_seq;
+      Tile t = tile_at(w->runs, w->j0);
+      int page = t.src == kPages ? row[t.y / kBN] : 0;
+      for (int j = 0; j < w->nt; ++j) {
+        const int s = issued % kStages;
+        // the next tile's page number is on its way while this one waits for its stage
+        Tile next = t;
+        int next_page = 0;
+        if (j + 1 < w->nt) {
+          next = tile_at(w->runs, w->j0 + j + 1);
+          if (next.src == kPages) next_page = row[next.y / kBN];
+        }
+        if (lane == 0 && issued >= kStages)
+          ok = tc::wait_bar(bar(empty0 + s), ((issued / kStages) - 1) & 1, c.status, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+        if (!ok) break;
+        const uint32_t dst = stage0 + s * kTile, fb = bar(full0 + s);
+        const int valid = t.src == kChunk ? w->n - t.y : kBN;
+        if (!is_k && valid < kBN) {
+          copy_ragged_tile(c.v + (static_cast<int64_t>(w->tok0 + t.y) * c.Hkv + w->g) * 256,
+                           static_cast<int64_t>(c.Hkv) * 256, valid, dst, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(fb);
+        } else if (lane == 0) {
+          mbar_expect_tx(fb, kTile);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t to = dst + h * kHalf;
+            if (t.src == kPages) tc::tma_3d(to, pages, 64 * h, 0, page * c.Hr + w->idx, fb);
+            else if (t.src == kSlots) tc::tma_3d(to, slots, 64 * h, t.y, w->slot * c.Hs + w->idx, fb);
+            else tc::tma_3d(to, chunk, 64 * h, w->g, w->tok0 + t.y, fb);
+          }
+        }
+        ++issued;
+        t = next;
+        page = next_page;
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) leave(p);
     }
     if (lane == 0) {  // nothing may still be landing in shared memory when the CTA ends
-      if (is_k) mbar_wait(bar(kBarQ), 0, c.status);
+      if (queries > 0) mbar_wait(bar(kBarQ), (queries - 1) & 1, c.status);
       tc::drain_loads(bar(full0), kStages, issued, c.status);
     }
-  } else if (warp == 1) {
+  } else {
     // ================= MMA issuer =================
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, false, false);
-      constexpr uint32_t kIdPV = tc::idesc_bf16(kBM, kD, false, true);
-      // operands lie below 256 KiB, so one at byte offset o is the base's descriptor + (o >> 4)
-      const uint64_t qd0 = tc::sdesc(sbase + kSmQ, 16, 1024), kd0 = tc::sdesc(sbase + kSmK, 16, 1024);
-      const uint64_t vd0 = tc::sdesc(sbase + kSmV, kHalf, 1024);
-      // S_t(j) = Q_t K_j^T, d 128 in 8 steps of 16
-      auto issue_s = [&](int t, int j) {
-        const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + (j % kKStages) * (kTile >> 4);
+    // The warp runs the loop as one, on values that are the same in all its lanes, and one
+    // elected lane issues: descriptors then stay in uniform registers.  (With lane 0 alone
+    // in the loop the tensor pipe waited for its issue: see the times above.)
+    constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, false, false);
+    constexpr uint32_t kIdPV = tc::idesc_bf16(kBM, kD, false, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // operands lie below 256 KiB, so one at byte offset o is the base's descriptor + (o >> 4)
+    const uint64_t qd0 = tc::sdesc(sbase + kSmQ, 16, 1024), kd0 = tc::sdesc(sbase + kSmK, 16, 1024);
+    const uint64_t vd0 = tc::sdesc(sbase + kSmV, kHalf, 1024);
+    auto wait = [&](int b, int phase) {
+      return __all_sync(0xffffffffu, tc::wait_bar(bar(b), phase & 1, c.status, abort_flag)) != 0;
+    };
+    // S_t = Q_t K^T with the K tile of stage s, d 128 in 8 steps of 16
+    auto issue_s = [&](int t, int s) {
+      const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + s * (kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          tc::mma_ss(tmem + kTmS + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
-        }
-        tc::commit(bar(kBarSFull + t));
-      };
-      // O_t += P_t(j) V_j, 128 keys in 8 steps of 16
-      auto issue_pv = [&](int t, int j) {
-        const uint64_t vd = vd0 + (j % kVStages) * (kTile >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ts(tmem + kTmO + t * 128, tmem + kTmS + t * 128 + kk * 8, vd + kk * (2048 >> 4), kIdPV,
-                     kk > 0 || j > 0 ? 1u : 0u);
-      };
-      bool ok = nt > 0 && tc::wait_bar(bar(kBarQ), 0, c.status, abort_flag) &&
-                tc::wait_bar(bar(kBarKFull), 0, c.status, abort_flag);
-      if (ok) {
-        tc::fence_after();
-        for (int t = 0; t < w.nq; ++t) issue_s(t, 0);
-        tc::commit(bar(kBarKEmpty));
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+        tc::mma_ss(tm + kTmS + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
       }
+      tc::commit(bar(kBarSFull + t));
+    };
+    // O_t (+)= P_t V with the V tile of stage s, 128 keys in 8 steps of 16
+    auto issue_pv = [&](int t, int s, bool first, int from, int to) {
+      const uint64_t vd = vd0 + s * (kTile >> 4);
+#pragma unroll
+      for (int kk = from; kk < to; ++kk)
+        tc::mma_ts(tm + kTmO + t * 128, tm + kTmS + t * 128 + kk * 8, vd + kk * (2048 >> 4), kIdPV,
+                   kk > 0 || !first ? 1u : 0u);
+    };
+    bool ok = true;
+    int k_tile = 0, v_tile = 0, p_tile[kQT] = {0, 0};
+    for (int p = 0;; ++p) {
+      const Piece *w = take(p, ok);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int nt = __shfl_sync(0xffffffffu, w->nt, 0), nq = __shfl_sync(0xffffffffu, w->nq, 0);
+      if (lane == 0) leave(p);
+      if (nt == 0) break;
+      ok = wait(kBarQ, p) && wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
+      if (!ok) break;
+      tc::fence_after();
+      if (tc::elect()) {
+        issue_s(0, k_tile % kKStages);
+        if (nq > 1) issue_s(1, k_tile % kKStages);
+        tc::commit(bar(kBarKEmpty + k_tile % kKStages));
+        if (nt == 1) tc::commit(bar(kBarQEmpty));
+      }
+      __syncwarp();
+      ++k_tile;
       for (int j = 0; j < nt && ok; ++j) {
-        for (int t = 0; t < w.nq && ok; ++t) {
-          ok = tc::wait_bar(bar(kBarPFull + t), j & 1, c.status, abort_flag);
-          if (ok && t == 0)
-            ok = tc::wait_bar(bar(kBarVFull + (j % kVStages)), (j / kVStages) & 1, c.status, abort_flag);
+#pragma unroll
+        for (int t = 0; t < kQT; ++t) {
+          if (t >= nq || !ok) break;
+          // K and V first: they are there long before P, and only P should be waited for
+          if (t == 0) ok = wait(kBarVFull + v_tile % kVStages, v_tile / kVStages);
+          if (ok && t == 0 && j + 1 < nt) ok = wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
+          if (ok) ok = wait(kBarPFull + t, p_tile[t]);
           if (!ok) break;
           tc::fence_after();
-          issue_pv(t, j);
-          if (t == w.nq - 1) tc::commit(bar(kBarVEmpty + (j % kVStages)));
-          if (j + 1 == nt) {
-            tc::commit(bar(kBarOFull + t));
-            continue;
+          if (tc::elect()) issue_pv(t, v_tile % kVStages, j == 0, 0, kPFirst / 16);
+          __syncwarp();
+          ok = wait(kBarPRest + t, p_tile[t]);
+          ++p_tile[t];
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect()) {
+            issue_pv(t, v_tile % kVStages, false, kPFirst / 16, 8);
+            if (t == nq - 1) tc::commit(bar(kBarVEmpty + v_tile % kVStages));
+            if (j + 1 == nt) {
+              tc::commit(bar(kBarOFull + t));
+            } else {
+              issue_s(t, k_tile % kKStages);
+              if (t == nq - 1) {
+                tc::commit(bar(kBarKEmpty + k_tile % kKStages));
+                if (j + 2 == nt) tc::commit(bar(kBarQEmpty));
+              }
+            }
           }
-          if (t == 0) {
-            ok = tc::wait_bar(bar(kBarKFull + ((j + 1) % kKStages)), ((j + 1) / kKStages) & 1, c.status, abort_flag);
-            if (!ok) break;
-            tc::fence_after();
+          __syncwarp();
+          if (t == nq - 1) {
+            ++v_tile;
+            if (j + 1 < nt) ++k_tile;
           }
-          issue_s(t, j + 1);
-          if (t == w.nq - 1) tc::commit(bar(kBarKEmpty + ((j + 1) % kKStages)));
         }
       }
-      // every MMA issued has completed before TMEM is freed
+    }
+    // every MMA issued has completed before TMEM is freed
+    if (tc::elect()) {
       tc::commit(bar(kBarDrain));
       mbar_wait(bar(kBarDrain), 0, c.status);
     }
-  } else if (warp >= kSoftWarp0 && (warp - kSoftWarp0) / 4 < w.nq) {
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ================= softmax of query tile qt: one thread per query row =================
     constexpr float kSlack = 8.0f;
     const int qt = (warp - kSoftWarp0) >> 2, row = ((warp & 3) << 5) | lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) << 5) << 16);
     const uint32_t s_cols = lane_base + kTmS + qt * 128, o_cols = lane_base + kTmO + qt * 128;
-    const int rpos = w.r0 + qt * w.npos + row / c.G;  // position of the row in the chunk
-    const int i = w.len + rpos;                       // and in the sequence
     const float scale = c.scale_log2;
-    float m = -INFINITY, l = 0.f;
     bool ok = true;
+    int s_tile = 0, done = 0;  // tiles and pieces of this query tile so far
+    for (int p = 0;; ++p) {
+      const Piece *w = take(p, ok);
+      if (!__all_sync(0xffffffffu, ok) || w->nt == 0) break;
+      if (qt >= w->nq) {
+        __syncwarp();
+        if (lane == 0) leave(p);
+        continue;
+      }
+      const int len = w->len, n = w->n, nt = w->nt, retr = w->retr;
+      const int rpos = w->r0 + qt * npos + row / c.G;  // position of the row in the chunk
+      const int i = len + rpos;                        // and in the sequence
+      float m = -INFINITY, l = 0.f;
+      const PrefillRun *run = w->runs;
+      int skip = w->j0;
+      for (; skip >= run->count; ++run) skip -= run->count;
+      Tile next = {run->src, (run->first + skip) * kBN};
+      int left = run->count - skip;
 
-    for (int j = 0; j < nt; ++j) {
-      // columns of the tile that this row sees; most tiles are seen whole
-      const Tile t = tile_at(runs, j0 + j);
-      const int base = w.len + t.y, end = min(i - base + 1, w.n - t.y);  // of a chunk tile
-      const bool whole = t.src == kPages   ? t.y + kBN <= w.len
-                         : t.src == kChunk ? end >= kBN && (w.retr || base + kBN <= c.S || i - c.W < base)
-                                           : false;
-      uint32_t vis[4] = {0u, 0u, 0u, 0u};
-      if (!whole) {
-        if (t.src == kPages) {
-          add_columns(vis, 0, w.len - t.y);
-        } else if (t.src == kSlots) {
-          const RingView v = ring_view(i, w.len, c.S, c.W);
-          add_columns(vis, 0, min(c.S, w.len) - t.y);
-          add_columns(vis, v.lo1 - t.y, v.hi1 - t.y);
-          add_columns(vis, v.lo2 - t.y, v.hi2 - t.y);
-        } else if (w.retr) {
-          add_columns(vis, 0, end);
-        } else {
-          add_columns(vis, 0, min(end, c.S - base));
-          add_columns(vis, i - c.W + 1 - base, end);
-        }
-      }
-
-      if (ok) ok = tc::wait_bar(bar(kBarSFull + qt), j & 1, c.status, abort_flag);
-      tc::fence_after();
-      float v[128];
-      load_row(s_cols, v);
-      if (!whole) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e) v[e] = (vis[e >> 5] >> (e & 31)) & 1u ? v[e] : -INFINITY;
-      }
-      const float tmax = largest(v) * scale;  // -inf when the row sees nothing of the tile
-      const bool need = tmax > m + kSlack;
-      float alpha = 1.f;
-      if (need) {
-        alpha = ex2(m - tmax);  // 0 while m is -inf
-        m = tmax;
-      }
-      if (j >= 1 && __any_sync(0xffffffffu, need)) {
-        // S_t(j) has landed, so P_t(j-1) V_{j-1} has too: rescale O_t in place
-#pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
-          float x[16];
-          tc::ld<16>(o_cols + 16 * q, x);
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * alpha);
-          tc::st16(o_cols + 16 * q, u);
-        }
-        tc::st_wait();
-      }
-      const float mc = m == -INFINITY ? 0.f : m;  // masked logits are -inf and give 0
-      float sum = probabilities<0>(v, scale, mc, s_cols) + probabilities<1>(v, scale, mc, s_cols);
-      sum += probabilities<2>(v, scale, mc, s_cols) + probabilities<3>(v, scale, mc, s_cols);
-      tc::st_wait();
-      tc::fence_before();
-      mbar_arrive_warp(bar(kBarPFull + qt));
-      l = fmaf(l, alpha, sum);
-    }
-    if (nt > 0 && ok) ok = tc::wait_bar(bar(kBarOFull + qt), 0, c.status, abort_flag);
-    tc::fence_after();
-    const bool live = row < c.G * w.npos && rpos < w.n;
-    if (w.segs > 1) {
-      // a segment's row as it is; it may have seen nothing (m = -inf, l = 0)
-      float *part = c.partials + (static_cast<int64_t>(w.item + w.seg) * kPrefillRows + qt * kBM + row) * kPrefillRow;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        float x[32];
-        tc::ld<32>(o_cols + 32 * q, x);
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(part + 32 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        }
-      }
-      if (live) *reinterpret_cast<float2 *>(part + kD) = make_float2(m, l);
-    } else {
-      const int64_t at = static_cast<int64_t>(w.tok0 + rpos) * c.Hq + w.g * c.G + row % c.G;
-      const float inv = 1.f / l;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        float x[32];
-        tc::ld<32>(o_cols + 32 * q, x);
-        if (live) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * u + 2 * e] * inv, x[8 * u + 2 * e + 1] * inv);
-              p[e] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            *reinterpret_cast<uint4 *>(c.out + at * (kD * 2) + q * 64 + u * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+      for (int j = 0; j < nt; ++j) {
+        // columns of the tile that this row sees; most tiles are seen whole
+        const Tile t = next;
+        const int base = len + t.y, end = min(i - base + 1, n - t.y);  // of a chunk tile
+        const bool whole = t.src == kPages   ? t.y + kBN <= len
+                           : t.src == kChunk ? end >= kBN && (retr || base + kBN <= c.S || i - c.W < base)
+                                             : false;
+        uint32_t vis[4] = {0u, 0u, 0u, 0u};
+        if (!whole) {
+          if (t.src == kPages) {
+            add_columns(vis, 0, len - t.y);
+          } else if (t.src == kSlots) {
+            const PrefillRing v = prefill_ring(i, len, c.S, c.W);
+            add_columns(vis, 0, min(c.S, len) - t.y);
+            add_columns(vis, v.lo1 - t.y, v.hi1 - t.y);
+            add_columns(vis, v.lo2 - t.y, v.hi2 - t.y);
+          } else if (retr) {
+            add_columns(vis, 0, end);
+          } else {
+            add_columns(vis, 0, min(end, c.S - base));
+            add_columns(vis, i - c.W + 1 - base, end);
           }
         }
+
+        if (--left > 0) {
+          next.y += kBN;
+        } else if (j + 1 < nt) {
+          ++run;
+          left = run->count;
+          next = {run->src, run->first * kBN};
+        }
+
+        if (ok) ok = tc::wait_bar(bar(kBarSFull + qt), s_tile & 1, c.status, abort_flag);
+        ++s_tile;
+        tc::fence_after();
+        float v[128];
+        load_row(s_cols, v);
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) v[e] = (vis[e >> 5] >> (e & 31)) & 1u ? v[e] : -INFINITY;
+        }
+        // Weights relative to the reference m so far, their largest logit beside them; when
+        // it passes m by 2^8 (rare after the first tiles) m moves, O_t and l are rescaled and
+        // the weights are done again.  S_t(j) has landed, so P_t(j-1) V_{j-1} has too and O_t
+        // may be rescaled in place.
+        float alpha = 1.f, sum;
+        if (j == 0) m = largest(v) * scale;  // -inf when the row sees nothing of the tile
+        while (true) {
+          const float mc = m == -INFINITY ? 0.f : m;  // masked logits are -inf and give 0
+          sum = probabilities<0>(v, scale, mc, s_cols) + probabilities<1>(v, scale, mc, s_cols);
+          sum += probabilities<2>(v, scale, mc, s_cols);
+          const float tmax = largest(v) * scale;
+          const bool need = tmax > m + kSlack;
+          if (!__any_sync(0xffffffffu, need)) break;
+          const float a = need ? ex2(m - tmax) : 1.f;  // 0 while m is -inf
+          if (need) m = tmax;
+          alpha *= a;
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            float x[16];
+            tc::ld<16>(o_cols + 16 * q, x);
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * a);
+            tc::st16(o_cols + 16 * q, u);
+          }
+        }
+        tc::st_wait();
+        tc::fence_before();
+        mbar_arrive_warp(bar(kBarPFull + qt));
+        sum += probabilities<3>(v, scale, m == -INFINITY ? 0.f : m, s_cols);
+        tc::st_wait();
+        tc::fence_before();
+        mbar_arrive_warp(bar(kBarPRest + qt));
+        l = fmaf(l, alpha, sum);
       }
-      if (live && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
+      const int part = w->part, tok = w->tok0 + rpos, head = w->g * c.G + row % c.G;
+      const bool live = row < c.G * npos && rpos < n;
+      __syncwarp();
+      if (lane == 0) leave(p);
+      if (ok) ok = tc::wait_bar(bar(kBarOFull + qt), done & 1, c.status, abort_flag);
+      ++done;
+      tc::fence_after();
+      if (part >= 0) {
+        // a piece's row as it is; it may have seen nothing (m = -inf, l = 0)
+        float *to = c.partials + (static_cast<int64_t>(part) * kPrefillRows + qt * kBM + row) * kPrefillRow;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float x[32];
+          tc::ld<32>(o_cols + 32 * q, x);
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(to + 32 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        }
+        if (live) *reinterpret_cast<float2 *>(to + kD) = make_float2(m, l);
+      } else {
+        const int64_t at = static_cast<int64_t>(tok) * c.Hq + head;
+        const float inv = 1.f / l;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float x[32];
+          tc::ld<32>(o_cols + 32 * q, x);
+          if (live) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t b16[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * u + 2 * e] * inv, x[8 * u + 2 * e + 1] * inv);
+                b16[e] = *reinterpret_cast<const uint32_t *>(&b);
+              }
+              *reinterpret_cast<uint4 *>(c.out + at * (kD * 2) + q * 64 + u * 16) =
+                  make_uint4(b16[0], b16[1], b16[2], b16[3]);
+            }
+          }
+        }
+        if (live && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
+      }
+      // O_t has been read: ordered before the next piece's first P_t, which frees it
+      tc::fence_before();
     }
   }
 

@@ -50,9 +50,9 @@ bool pool_layout(int layers, int Hkv, int Hq, const uint8_t *mask, int S, int W,
   };
   L->status = take(256);
   L->counters = take(static_cast<size_t>(L->max_items) * 4);
-  // decode segments, or pre-fill segments (calls on a pool are ordered: one area serves both)
+  // decode segments, or pre-fill pieces (calls on a pool are ordered: one area serves both)
   L->partials = take(std::max((static_cast<size_t>(kMaxCtas) + L->max_items) * G * kPartRow * 4,
-                              static_cast<size_t>(kPrefillSegs) * kPrefillRows * kPrefillRow * 4));
+                              static_cast<size_t>(kPrefillParts) * kPrefillRows * kPrefillRow * 4));
   L->layers = take(static_cast<size_t>(layers) * sizeof(PoolLayerDesc));
   L->table = take(static_cast<size_t>(max_seqs) * L->pages_per_seq * 4);
   const double est = static_cast<double>(num_pages) * layers * Hkv * kPoolTile * page_row * 2 +

@@ -56,12 +56,76 @@ duo_status pool_init(duo_pool *P, cudaStream_t st);
 constexpr int kPrefillMaxTokens = 1 << 18;  // tokens of one call
 // pages that a call's tokens can touch: theirs, and a partial one at either end of each
 constexpr int kPrefillMaxPages = kPrefillMaxTokens / kPoolTile + 2 * kPoolMaxSeqs;
-constexpr int kPrefillRows = 256;           // query rows of a CTA (two tensor-core tiles)
-constexpr int kPrefillSegs = 160;           // key segments whose partial rows fit the scratch
+constexpr int kPrefillRows = 256;           // query rows of an item (two tensor-core tiles)
+constexpr int kPrefillCtas = 148;           // CTAs of the attention launch, one per SM
+constexpr int kPrefillParts = 2 * kPrefillCtas;  // pieces of cut items: a CTA's first and last
 constexpr int kPrefillRow = 132;            // floats of a partial row: 128 sums, max, sum of weights, 2 unused
+constexpr int kPrefillMaxRuns = 5;
 
-// The attention launch.  Sequences are listed by decreasing work per CTA; CTAs of
-// retrieval heads come first.
+// Where an item's key tiles come from: the sequence's pages, its sinks and ring in slot
+// order, the call's own rows.
+enum PrefillSource { kPages, kSlots, kChunk };
+// Consecutive key tiles (of 128) of one source.
+struct PrefillRun {
+  int src, first, count;
+};
+
+// Slot order: slot x < S holds position x; ring slot S + y holds the newest position
+// p = y (mod W) below len, that is, with r = len mod W, len - r + y for y < r and
+// len - r - W + y for y >= r, where it is at least S.  Query i sees it iff i - p < W.  So
+// with a = i - len + r + 1 and e = S - len + r + W the visible ring slots of i are
+//   y in [max(0, a - W, e - W), r)  and  y in [max(r, a, e), W).
+struct PrefillRing {
+  int lo1, hi1, lo2, hi2;  // slots (S + y)
+};
+__host__ __device__ inline int larger(int a, int b) { return a > b ? a : b; }
+__host__ __device__ inline int smaller(int a, int b) { return a < b ? a : b; }
+__host__ __device__ inline PrefillRing prefill_ring(int i, int len, int S, int W) {
+  const int r = len % W, a = i - len + r + 1, e = S - len + r + W;
+  return {S + larger(0, larger(a, e) - W), S + r, S + larger(r, larger(a, e)), S + W};
+}
+// Appends the tiles that meet rows [lo, hi) of a source, from tile `at` on.
+__host__ __device__ inline void add_run(PrefillRun *runs, int &k, int &at, int src, int lo, int hi) {
+  if (lo >= hi) return;
+  const int a = larger(lo / kPoolTile, at), b = (hi + kPoolTile - 1) / kPoolTile;
+  if (a < b) {
+    runs[k++] = {src, a, b - a};
+    at = b;
+  }
+}
+// The key tiles of the item whose first query is position r0 of the sequence's n new
+// ones, npos positions a query tile; returns how many runs.  Streaming heads skip tiles
+// that hold no position visible to any of the queries; the first one reaches back
+// furthest.
+__host__ __device__ inline int prefill_runs(bool retr, int len, int n, int r0, int npos, int S, int W,
+                                            PrefillRun *runs) {
+  const int rows = smaller(r0 + 2 * npos, n);  // positions 0 .. rows-1 of the chunk are needed
+  int k = 0, at = 0;
+  if (retr) {
+    add_run(runs, k, at, kPages, 0, len);
+    at = 0;
+    add_run(runs, k, at, kChunk, 0, rows);
+    return k;
+  }
+  const PrefillRing v = prefill_ring(len + r0, len, S, W);
+  add_run(runs, k, at, kSlots, 0, smaller(S, len));
+  add_run(runs, k, at, kSlots, v.lo1, v.hi1);
+  add_run(runs, k, at, kSlots, v.lo2, v.hi2);
+  at = 0;
+  add_run(runs, k, at, kChunk, 0, smaller(rows, S - len));
+  add_run(runs, k, at, kChunk, larger(0, r0 - W + 1), rows);
+  return k;
+}
+
+// A CTA's part of the items that are cut: `tiles` key tiles from tile `tile` of item
+// `item` on.  Partial rows of its first item go to place `part`, of its last to part + 1.
+struct PrefillShare {
+  int item, tile, tiles, part;
+};
+
+// The attention launch.  Sequences are listed by decreasing work per item; retrieval heads'
+// items come first.  CTA c works on items c, c + grid, ... below whole_items, then on its
+// share of the others.
 struct PoolPrefillCall {
   CUtensorMap tm_q, tm_k, tm_v;  // q [tokens][Hq][d], k and v [tokens][Hkv][d]
   const PoolLayerDesc *layer;    // device
@@ -71,15 +135,14 @@ struct PoolPrefillCall {
   char *out;
   float *lse, *partials;
   uint32_t *status;
-  int nseq, Hq, Hkv, G, S, W, Hr, Hs, retr_ctas, ctas;
+  int nseq, Hq, Hkv, G, S, W, Hr, Hs, retr_items, whole_items, ctas;
   float scale_log2;
   int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
   int tok0[kPoolMaxSeqs];        // first of the sequence's tokens in the call's tensors
-  int segs[kPoolMaxSeqs];        // key segments of each of its retrieval CTAs' rows
-  int seg0[kPoolMaxSeqs];        // its first partial segment (segs > 1)
-  int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // CTAs before a sequence, per kind
+  int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // items before a sequence, per kind
+  PrefillShare share[kPrefillCtas];
 };
-// Positions per query tile and CTAs (of two tiles) that cover n positions of one KV head.
+// Positions per query tile and items (of two tiles) that cover n positions of one KV head.
 inline int prefill_tile_positions(int G) { return 128 / G; }
 inline int prefill_blocks(int n, int G) {
   const int per = 2 * prefill_tile_positions(G);

@@ -2,9 +2,9 @@
 // attention is k_prefill_pool_tc.cu; here are the plan of a call, and its last launch,
 // which joins split rows and appends the tokens.
 //
-// A row whose keys were split into segments with partial sums O_s, maxima m_s (base 2) and
+// A row whose keys were cut into pieces with partial sums O_s, maxima m_s (base 2) and
 // weights l_s is O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max m_s, lse = (M +
-// log2 of the denominator) ln 2; segments in order, so a result does not depend on timing.
+// log2 of the denominator) ln 2; pieces in order, so a result does not depend on timing.
 #include <cmath>
 #include <exception>
 
@@ -16,6 +16,12 @@ namespace duo {
 
 namespace {
 
+// An item whose key tiles several CTAs share: its query rows and the places of its pieces
+// in the scratch, part0, part1, part1 + 2, ...
+struct PrefillCut {
+  int seq, block, head, pieces, part0, part1;
+};
+
 // The call's last launch, sequences in the caller's order.
 struct PoolFinishCall {
   const PoolLayerDesc *layer;
@@ -25,13 +31,11 @@ struct PoolFinishCall {
   char *out;
   float *lse;
   const float *partials;
-  int nseq, tokens, Hq, Hkv, G, S, W, Hr, npos, npages;
-  int64_t join_rows;
+  int nseq, tokens, Hq, Hkv, G, S, W, npos, npages, ncuts;
   int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
   int tok0[kPoolMaxSeqs + 1];
   int page0[kPoolMaxSeqs + 1];  // a sequence's entries in `pages`, from logical page len / 128 on
-  int segs[kPoolMaxSeqs], seg0[kPoolMaxSeqs];
-  int join0[kPoolMaxSeqs + 1];  // rows to join before a sequence's
+  PrefillCut cuts[kPrefillCtas];
   int pages[kPrefillMaxPages];
 };
 
@@ -46,32 +50,30 @@ __device__ __forceinline__ int find(const int *first, int n, int x) {
   return lo;
 }
 
-// One warp per split row: weights of its segments over the lanes, then four dimensions a
-// lane, eight segments' loads in flight.
-__device__ __forceinline__ void join_row(const PoolFinishCall &c, const PoolLayerDesc &L, int r, int lane) {
-  const int s = find(c.join0, c.nseq, r);
-  int rem = r - c.join0[s];
-  const int gq = rem % c.G;
-  rem /= c.G;
-  const int h = rem % c.Hr, pos = rem / c.Hr;
-  const int block = pos / (2 * c.npos), in = pos % (2 * c.npos), segs = c.segs[s];
-  const int row = in / c.npos * 128 + in % c.npos * c.G + gq;
-  const float *part = c.partials +
-                      (static_cast<int64_t>(c.seg0[s] + (block * c.Hr + h) * segs) * kPrefillRows + row) * kPrefillRow;
-  constexpr int64_t kSeg = static_cast<int64_t>(kPrefillRows) * kPrefillRow;
-  constexpr int kPer = kPrefillSegs / 32;
+// One warp per row of a cut item: weights of its pieces over the lanes, then four
+// dimensions a lane, eight pieces' loads in flight.
+__device__ __forceinline__ void join_row(const PoolFinishCall &c, int r, int lane) {
+  const PrefillCut &cut = c.cuts[r / kPrefillRows];
+  const int row = r % kPrefillRows, in = row % 128, segs = cut.pieces;
+  const int pos = cut.block * 2 * c.npos + row / 128 * c.npos + in / c.G;
+  if (in >= c.G * c.npos || pos >= c.n[cut.seq]) return;
+  auto part = [&](int seg) {
+    const int at = seg == 0 ? cut.part0 : cut.part1 + 2 * (seg - 1);
+    return c.partials + (static_cast<int64_t>(at) * kPrefillRows + row) * kPrefillRow;
+  };
+  constexpr int kPer = (kPrefillCtas + 31) / 32;
   float w[kPer], m = -INFINITY, l = 0.f;
   float2 ml[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int seg = lane + 32 * i;
-    ml[i] = seg < segs ? *reinterpret_cast<const float2 *>(part + seg * kSeg + 128) : make_float2(-INFINITY, 0.f);
+    ml[i] = seg < segs ? *reinterpret_cast<const float2 *>(part(seg) + 128) : make_float2(-INFINITY, 0.f);
     m = fmaxf(m, ml[i].x);
   }
   m = warp_max(m);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    // a segment that the row saw nothing of has no sum (its O was never written)
+    // a piece that the row saw nothing of has no weight
     w[i] = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - m);
     l = fmaf(ml[i].y, w[i], l);
   }
@@ -86,7 +88,7 @@ __device__ __forceinline__ void join_row(const PoolFinishCall &c, const PoolLaye
       for (int e = 0; e < 8; ++e) {
         const int seg = 32 * i + b + e;
         ws[e] = __shfl_sync(0xffffffffu, w[i], b + e);
-        x[e] = seg < segs && ws[e] != 0.f ? *reinterpret_cast<const float4 *>(part + seg * kSeg + 4 * lane)
+        x[e] = seg < segs && ws[e] != 0.f ? *reinterpret_cast<const float4 *>(part(seg) + 4 * lane)
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
@@ -99,14 +101,14 @@ __device__ __forceinline__ void join_row(const PoolFinishCall &c, const PoolLaye
     }
   }
   const float inv = 1.f / l;
-  const int64_t at = static_cast<int64_t>(c.tok0[s] + pos) * c.Hq + L.hm.retr_head[h] * c.G + gq;
+  const int64_t at = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + in % c.G;
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
   reinterpret_cast<uint2 *>(c.out + at * 256)[lane] =
       make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
   if (lane == 0 && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
 }
 
-// Warps: one per split row; then one per (token, KV head), K on the lower lanes, V on the
+// Warps: one per row of the cut items; then one per (token, KV head), K on the lower lanes, V on the
 // upper; then one per (sequence, retrieval head) for the rest of a page that the call
 // opened, and the block-table entries.
 __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_constant__ PoolFinishCall c) {
@@ -114,8 +116,9 @@ __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_c
   int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const PoolLayerDesc &L = *c.layer;
-  if (w < c.join_rows) return join_row(c, L, static_cast<int>(w), lane);
-  w -= c.join_rows;
+  const int64_t join_rows = static_cast<int64_t>(c.ncuts) * kPrefillRows;
+  if (w < join_rows) return join_row(c, static_cast<int>(w), lane);
+  w -= join_rows;
   if (w < static_cast<int64_t>(c.tokens) * c.Hkv) {
     const int t = static_cast<int>(w / c.Hkv), g = static_cast<int>(w % c.Hkv), idx = L.hm.kind_idx[g];
     const int s = find(c.tok0, c.nseq, t), pos = c.len[s] + t - c.tok0[s], end = c.len[s] + c.n[s];
@@ -153,32 +156,68 @@ __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_c
   }
 }
 
-// Splits the keys of retrieval CTAs into segments: segs[s] per CTA of sequence s.  `tiles`
-// and `ctas` are its key tiles and its CTAs, streaming CTAs run beside them.  With fewer
-// CTAs than SMs, the shortest segments that still give every CTA an SM of its own; with
-// more, only what is longer than an SM's even share.  A segment has at least four tiles
-// (its start and its partial rows cost about two), and all segments of split rows fit
-// the scratch.
-void plan_segments(const std::vector<int64_t> &tiles, const std::vector<int64_t> &ctas, int64_t streaming_ctas,
-                   int num_sms, std::vector<int> *segs) {
-  const size_t n = tiles.size();
-  int64_t retr_ctas = 0, work = 0;
-  for (size_t s = 0; s < n; ++s) {
-    retr_ctas += ctas[s];
-    work += ctas[s] * tiles[s];
-  }
-  segs->assign(n, 1);
-  if (retr_ctas == 0) return;
-  const int64_t sms = std::max<int64_t>(num_sms - streaming_ctas, num_sms / 2);
-  for (int64_t target = std::max<int64_t>(4, (work + sms - 1) / sms);; target += std::max<int64_t>(1, target / 16)) {
-    int64_t all = 0, split = 0;
-    for (size_t s = 0; s < n; ++s) {
-      const int64_t k = (tiles[s] + target - 1) / target;
-      (*segs)[s] = static_cast<int>(std::min<int64_t>(k, kPrefillSegs + 1));
-      all += ctas[s] * k;
-      split += k > 1 ? ctas[s] * k : 0;
+// Deals the items out, `tiles` key tiles each: whole ones in rounds, item r * ctas + c to
+// CTA c, as long as no CTA gets more than its even share, so that neighbours read the same
+// keys at about the same time; then the rest, cut where a CTA's share is full.  An item
+// costs a CTA about two tiles more than its tiles (queries, the first product, its rows'
+// way out, in pieces their way through the scratch); pieces of fewer than two tiles are
+// avoided, and a short call runs on as many CTAs as have four tiles each.
+struct Deal {
+  int whole = 0, ctas = 1;
+  std::vector<PrefillShare> share;
+  struct Cut {
+    int item, pieces, part0, part1;
+  };
+  std::vector<Cut> cuts;
+};
+void deal_items(const std::vector<int> &tiles, int sms, Deal *d) {
+  constexpr int kItemCost = 2, kLeast = 2, kShareTiles = 4;
+  const int items = static_cast<int>(tiles.size());
+  int64_t total = 0;
+  for (int t : tiles) total += t;
+  d->ctas = static_cast<int>(std::min<int64_t>(std::min(sms, kPrefillCtas), std::max<int64_t>(1, total / kShareTiles)));
+  const int ctas = d->ctas;
+  total += static_cast<int64_t>(items) * kItemCost;
+  std::vector<int64_t> load(ctas);
+  for (int64_t even = (total + ctas - 1) / ctas;;) {
+    std::fill(load.begin(), load.end(), 0);
+    int u = 0;
+    for (bool fits = true; fits && u + ctas <= items;) {
+      for (int c = 0; c < ctas; ++c) fits &= load[c] + tiles[u + c] + kItemCost <= even;
+      if (!fits) break;
+      for (int c = 0; c < ctas; ++c) load[c] += tiles[u + c] + kItemCost;
+      u += ctas;
     }
-    if (split <= kPrefillSegs && (retr_ctas >= sms || all <= sms)) return;
+    d->whole = u;
+    d->share.assign(ctas, PrefillShare{0, 0, 0, 0});
+    d->cuts.clear();
+    int rank = 0;
+    int t0 = 0;  // tiles of item u already dealt
+    for (int c = 0; c < ctas && u < items; ++c) {
+      int64_t room = even - load[c];
+      PrefillShare &sh = d->share[c];
+      sh = {u, t0, 0, 2 * rank};
+      while (u < items) {
+        const int rest = tiles[u] - t0;
+        const int64_t can = room - kItemCost;
+        if (can < std::min(rest, kLeast)) break;
+        int take = static_cast<int>(std::min<int64_t>(rest, can));
+        if (rest - take < kLeast) take = rest;
+        if (t0 > 0) ++d->cuts.back().pieces;
+        else if (take < rest) d->cuts.push_back({u, 1, sh.item == u ? sh.part : sh.part + 1, 2 * (rank + 1)});
+        sh.tiles += take;
+        room -= take + kItemCost;
+        t0 += take;
+        if (t0 < tiles[u]) break;
+        ++u;
+        t0 = 0;
+      }
+      if (sh.tiles > 0) ++rank;
+    }
+    if (u == items) return;
+    int64_t rest = -t0;
+    for (int i = u; i < items; ++i) rest += tiles[i] + kItemCost;
+    even += std::max<int64_t>(1, rest / ctas);
   }
 }
 
@@ -193,9 +232,8 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     tokens += n[i];
   }
   if (tokens > kPrefillMaxTokens) return DUO_ERR_INVALID;
-  std::vector<int64_t> need(nseq), tiles(nseq), ctas(nseq);
+  std::vector<int64_t> need(nseq), tiles(nseq);
   const int Hr = P->hr[layer], Hs = P->hs[layer];
-  int64_t streaming = 0;
   for (int i = 0; i < nseq; ++i) {
     const int64_t len = P->len[seqs[i]][layer], end = len + n[i];
     if (end > P->max_len) return DUO_ERR_CAPACITY;
@@ -203,17 +241,14 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     fresh += std::max<int64_t>(0, need[i] - static_cast<int64_t>(P->pages[seqs[i]].size()));
     entries += need[i] - len / kPoolTile;
     tiles[i] = (len + kPoolTile - 1) / kPoolTile + (n[i] + kPoolTile - 1) / kPoolTile;
-    ctas[i] = static_cast<int64_t>(prefill_blocks(n[i], P->G)) * Hr;
-    streaming += static_cast<int64_t>(prefill_blocks(n[i], P->G)) * Hs;
   }
   if (fresh > static_cast<int64_t>(P->free_pages.size())) return DUO_ERR_CAPACITY;
   const duo_status r = pool_init(P, st);
   if (r != DUO_OK) return r;
 
-  std::vector<int> segs, order(nseq);
-  plan_segments(tiles, ctas, streaming, P->num_sms, &segs);
+  std::vector<int> order(nseq);
   for (int i = 0; i < nseq; ++i) order[i] = i;
-  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return tiles[a] * segs[b] > tiles[b] * segs[a]; });
+  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return tiles[a] > tiles[b]; });
 
   PoolPrefillCall a{};
   PoolFinishCall f{};
@@ -233,46 +268,65 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   a.G = f.G = P->G;
   a.S = f.S = P->S;
   a.W = f.W = P->W;
-  a.Hr = f.Hr = Hr;
+  a.Hr = Hr;
   a.Hs = Hs;
   a.scale_log2 = P->scale * kLog2e;
   f.tokens = static_cast<int>(tokens);
   f.npos = prefill_tile_positions(P->G);
   f.npages = static_cast<int>(entries);
-  int tok = 0, page = 0, seg = 0, join = 0;
+  int tok = 0, page = 0;
   for (int i = 0; i < nseq; ++i) {
     f.slot[i] = seqs[i];
     f.len[i] = static_cast<int>(P->len[seqs[i]][layer]);
     f.n[i] = n[i];
     f.tok0[i] = tok;
     f.page0[i] = page;
-    f.segs[i] = segs[i];
-    f.seg0[i] = seg;
-    f.join0[i] = join;
     tok += n[i];
     page += static_cast<int>(need[i] - f.len[i] / kPoolTile);
-    if (segs[i] > 1) {
-      seg += static_cast<int>(ctas[i]) * segs[i];
-      join += n[i] * Hr * P->G;
-    }
   }
   f.tok0[nseq] = tok;
   f.page0[nseq] = page;
-  f.join0[nseq] = join;
-  f.join_rows = join;
+  std::vector<int> item_tiles;
+  for (int kind = 0; kind < 2; ++kind) {  // retrieval heads' items, then streaming heads'
+    const int heads = kind == 0 ? Hr : Hs;
+    int *first = kind == 0 ? a.rfirst : a.sfirst;
+    for (int i = 0; i < nseq; ++i) {
+      const int s = order[i], blocks = prefill_blocks(n[s], P->G);
+      first[i + 1] = first[i] + blocks * heads;
+      for (int b = blocks - 1; b >= 0 && heads > 0; --b) {
+        PrefillRun runs[kPrefillMaxRuns];
+        const int k = prefill_runs(kind == 0, f.len[s], n[s], b * 2 * f.npos, f.npos, P->S, P->W, runs);
+        int t = 0;
+        for (int r = 0; r < k; ++r) t += runs[r].count;
+        item_tiles.insert(item_tiles.end(), heads, t);
+      }
+    }
+  }
   for (int i = 0; i < nseq; ++i) {
-    const int s = order[i], blocks = prefill_blocks(n[s], P->G);
+    const int s = order[i];
     a.slot[i] = f.slot[s];
     a.len[i] = f.len[s];
     a.n[i] = f.n[s];
     a.tok0[i] = f.tok0[s];
-    a.segs[i] = f.segs[s];
-    a.seg0[i] = f.seg0[s];
-    a.rfirst[i + 1] = a.rfirst[i] + blocks * Hr * f.segs[s];
-    a.sfirst[i + 1] = a.sfirst[i] + blocks * Hs;
   }
-  a.retr_ctas = a.rfirst[nseq];
-  a.ctas = a.retr_ctas + a.sfirst[nseq];
+  a.retr_items = a.rfirst[nseq];
+  Deal deal;
+  deal_items(item_tiles, P->num_sms, &deal);
+  a.whole_items = deal.whole;
+  a.ctas = deal.ctas;
+  std::copy(deal.share.begin(), deal.share.end(), a.share);
+  f.ncuts = static_cast<int>(deal.cuts.size());
+  for (int i = 0; i < f.ncuts; ++i) {
+    const Deal::Cut &cut = deal.cuts[i];
+    const bool retr = cut.item < a.retr_items;
+    const int u = retr ? cut.item : cut.item - a.retr_items, heads = retr ? Hr : Hs;
+    const int *first = retr ? a.rfirst : a.sfirst;
+    const int at = static_cast<int>(std::upper_bound(first, first + nseq, u) - first) - 1;
+    const HeadMap &hm = P->h_layers[layer].hm;
+    const int rem = u - first[at];
+    f.cuts[i] = {order[at], prefill_blocks(n[order[at]], P->G) - 1 - rem / heads,
+                 retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1};
+  }
   if (!dry_run() && prepare_prefill_pool_tc(&a, q, k, v, f.tokens) != cudaSuccess) return DUO_ERR_CUDA;
   for (int i = 0; i < nseq; ++i) P->pages[seqs[i]].reserve(static_cast<size_t>(need[i]));
 
@@ -288,7 +342,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   if (e == cudaSuccess)
     e = launch_via_hook([&] {
       const int64_t tail = std::max<int64_t>(static_cast<int64_t>(nseq) * Hr, (f.npages + 31) / 32);
-      const int64_t warps = f.join_rows + tokens * P->Hkv + tail;
+      const int64_t warps = static_cast<int64_t>(f.ncuts) * kPrefillRows + tokens * P->Hkv + tail;
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
       cfg.blockDim = dim3(256);
