@@ -52,7 +52,8 @@ constexpr int kHalf = 16384;
 constexpr int kSmQ = 0, kSmK = kSmQ + kQT * kTile, kSmV = kSmK + kKStages * kTile, kSmBar = kSmV + kVStages * kTile;
 constexpr int kSmMisc = kSmBar + 256;
 constexpr int kPieces = 4;  // pieces listed ahead
-constexpr int kSmemAlloc = kSmMisc + 768 + 1024;  // slack for aligning the base to 1 KiB
+constexpr int kSmOut = kSmMisc + 768;  // per softmax warp: 32 rows' 32 dims on their way out
+constexpr int kSmemAlloc = kSmOut + 4 * kQT * 2048 + 1024;  // slack for aligning the base to 1 KiB
 constexpr int kTmS = 0, kTmO = 256;
 constexpr int kPFirst = 96;  // keys of a tile whose P is handed over first
 
@@ -112,14 +113,11 @@ __device__ __forceinline__ Tile tile_at(const PrefillRun *runs, int j) {
   return {runs->src, (runs->first + j) * kBN};
 }
 
-// columns [lo, hi) of a 128-column tile into a 128-bit mask
-__device__ __forceinline__ void add_columns(uint32_t (&m)[4], int lo, int hi) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int a = min(max(lo - 32 * k, 0), 32), b = min(max(hi - 32 * k, 0), 32);
-    const uint32_t below_a = a >= 32 ? ~0u : (1u << a) - 1u, below_b = b >= 32 ? ~0u : (1u << b) - 1u;
-    m[k] |= below_b & ~below_a;
-  }
+// bits below x (x <= 0: none, x >= 32: all)
+__device__ __forceinline__ uint32_t bits_below(int x) {
+  uint32_t r;
+  asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(r) : "r"(max(x, 0)));  // a shift by 32 or more gives 0
+  return ~r;
 }
 
 // 128 consecutive fp32 columns of this thread's lane; one wait that names every register,
@@ -228,6 +226,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
     *abort_flag = 0;
   }
   if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+  if (lane == 0 && (warp == 0 || warp == 2)) {
+    // the layer's maps live in device memory, written before this launch
+    const bool k = warp == 0;
+    for (const CUtensorMap *m : {k ? &L.tm_kr : &L.tm_vr, k ? &L.tm_ks : &L.tm_vs}) {
+      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
+      tc::prefetch_map(m);
+    }
+    if (k) tc::prefetch_map(&c.tm_q);
+    tc::prefetch_map(k ? &c.tm_k : &c.tm_v);
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -257,26 +265,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         mbar_arrive(bar(kBarPiece + p % kPieces));
         ++p;
       };
-      for (int u = blockIdx.x; u < c.whole_items; u += gridDim.x) {
-        Piece *w = slot();
-        if (!ok) break;
-        w->nt = item_of(c, L, u, *w);
-        w->j0 = 0;
-        w->part = -1;
-        publish();
-      }
       const PrefillShare sh = c.share[blockIdx.x];
-      int j0 = sh.tile, left = sh.tiles;
-      for (int u = sh.item; left > 0 && ok; ++u) {
+      int u = blockIdx.x, j0 = 0, left = sh.tiles;
+      while (ok) {
+        const bool whole = u < c.whole_items;
+        if (!whole && left == sh.tiles) {  // on to the share
+          u = sh.item;
+          j0 = sh.tile;
+        }
+        if (!whole && left == 0) break;
         Piece *w = slot();
         if (!ok) break;
-        const int tiles = item_of(c, L, u, *w), nt = min(tiles - j0, left);
+        const int tiles = item_of(c, L, u, *w), nt = whole ? tiles : min(tiles - j0, left);
         w->j0 = j0;
         w->nt = nt;
         w->part = nt == tiles ? -1 : (u == sh.item ? sh.part : sh.part + 1);
-        left -= nt;
-        j0 = 0;
         publish();
+        u += whole ? gridDim.x : 1;
+        if (!whole) {
+          left -= nt;
+          j0 = 0;
+        }
       }
       if (ok) {
         Piece *w = slot();
@@ -289,13 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
   } else if (warp == 0 || warp == 2) {
     // ================= producers: warp 0 Q and K, warp 2 V =================
     const bool is_k = warp == 0;
-    if (lane == 0) {
-      // the layer's maps live in device memory, written before this launch
-      const CUtensorMap *m = is_k ? &L.tm_kr : &L.tm_vr;
-      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
-      m = is_k ? &L.tm_ks : &L.tm_vs;
-      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
-    }
     const uint32_t stage0 = sbase + (is_k ? kSmK : kSmV);
     const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
     constexpr int kStages = kKStages;
@@ -305,18 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
     for (int p = 0;; ++p) {
       const Piece *w = take(p, ok);
       if (!__all_sync(0xffffffffu, ok) || w->nt == 0) break;
-      if (is_k) {
-        if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        if (lane == 0) {
-          mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
-          for (int t = 0; t < w->nq; ++t)
-            for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
-              tc::tma_3d(sbase + kSmQ + t * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G, w->tok0 + w->r0 + t * npos,
-                         bar(kBarQ));
-        }
-        ++queries;
-      }
       const CUtensorMap *pages = is_k ? &L.tm_kr : &L.tm_vr, *slots = is_k ? &L.tm_ks : &L.tm_vs;
       const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
       const int *row = c.table + static_cast<int64_t>(w->slot) * c.pages_per_seq;
@@ -354,6 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         ++issued;
         t = next;
         page = next_page;
+        if (is_k && j == 0) {  // the queries behind the first keys: their place is free later
+          if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
+            for (int q = 0; q < w->nq; ++q)
+              for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
+                tc::tma_3d(sbase + kSmQ + q * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G,
+                           w->tok0 + w->r0 + q * npos, bar(kBarQ));
+          }
+          ++queries;
+        }
       }
       if (!ok) break;
       __syncwarp();
@@ -486,30 +489,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
       for (; skip >= run->count; ++run) skip -= run->count;
       Tile next = {run->src, (run->first + skip) * kBN};
       int left = run->count - skip;
+      // Slots that row i sees: [0, front) and [ring.lo2, ring.hi2).  Either run of the ring
+      // starts at its first slot, and continues the sinks, or the other run is empty.
+      PrefillRing ring = prefill_ring(i, len, c.S, c.W);
+      int front = min(c.S, len);
+      if (ring.lo1 == c.S) {
+        front = max(front, ring.hi1);
+      } else {
+        ring.lo2 = ring.lo1;
+        ring.hi2 = ring.hi1;
+      }
 
       for (int j = 0; j < nt; ++j) {
         // columns of the tile that this row sees; most tiles are seen whole
         const Tile t = next;
-        const int base = len + t.y, end = min(i - base + 1, n - t.y);  // of a chunk tile
-        const bool whole = t.src == kPages   ? t.y + kBN <= len
-                           : t.src == kChunk ? end >= kBN && (retr || base + kBN <= c.S || i - c.W < base)
-                                             : false;
-        uint32_t vis[4] = {0u, 0u, 0u, 0u};
-        if (!whole) {
-          if (t.src == kPages) {
-            add_columns(vis, 0, len - t.y);
-          } else if (t.src == kSlots) {
-            const PrefillRing v = prefill_ring(i, len, c.S, c.W);
-            add_columns(vis, 0, min(c.S, len) - t.y);
-            add_columns(vis, v.lo1 - t.y, v.hi1 - t.y);
-            add_columns(vis, v.lo2 - t.y, v.hi2 - t.y);
-          } else if (retr) {
-            add_columns(vis, 0, end);
-          } else {
-            add_columns(vis, 0, min(end, c.S - base));
-            add_columns(vis, i - c.W + 1 - base, end);
+        // columns [0, front_t) and [from, to) of it
+        int front_t, from = 0, to = 0;
+        if (t.src == kPages) {
+          front_t = len - t.y;
+        } else if (t.src == kSlots) {
+          front_t = front - t.y;
+          from = ring.lo2 - t.y;
+          to = ring.hi2 - t.y;
+        } else {
+          const int base = len + t.y;
+          front_t = to = min(i - base + 1, n - t.y);
+          if (!retr) {
+            front_t = min(to, c.S - base);
+            from = i - c.W + 1 - base;
           }
         }
+        const bool whole = front_t >= kBN || (from <= max(front_t, 0) && to >= kBN);
 
         if (--left > 0) {
           next.y += kBN;
@@ -526,7 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         load_row(s_cols, v);
         if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e) v[e] = (vis[e >> 5] >> (e & 31)) & 1u ? v[e] : -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t vis = bits_below(front_t - 32 * k) | (bits_below(to - 32 * k) & ~bits_below(from - 32 * k));
+            if (vis != ~0u) {  // a warp's rows are few positions: most groups of 32 are seen whole
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[32 * k + e] = (vis >> e) & 1u ? v[32 * k + e] : -INFINITY;
+            }
+          }
         }
         // Weights relative to the reference m so far, their largest logit beside them; when
         // it passes m by 2^8 (rare after the first tiles) m moves, O_t and l are rescaled and
@@ -571,38 +587,49 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
       ++done;
       tc::fence_after();
       if (part >= 0) {
-        // a piece's row as it is; it may have seen nothing (m = -inf, l = 0)
-        float *to = c.partials + (static_cast<int64_t>(part) * kPrefillRows + qt * kBM + row) * kPrefillRow;
+        // a piece's rows as they are, 16 bytes of 128 rows side by side; a row may have seen
+        // nothing (m = -inf, l = 0)
+        float4 *to = reinterpret_cast<float4 *>(c.partials) + (part * kQT + qt) * (kPrefillRow / 4) * kBM + row;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float x[32];
           tc::ld<32>(o_cols + 32 * q, x);
-          if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(to + 32 * q + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-          }
+          for (int e = 0; e < 8; ++e)
+            to[(8 * q + e) * kBM] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
-        if (live) *reinterpret_cast<float2 *>(to + kD) = make_float2(m, l);
+        to[(kD / 4) * kBM] = make_float4(m, l, 0.f, 0.f);
       } else {
-        const int64_t at = static_cast<int64_t>(tok) * c.Hq + head;
+        const int64_t at = live ? static_cast<int64_t>(tok) * c.Hq + head : -1;
         const float inv = 1.f / l;
+        // through shared memory: a warp's store then covers eight rows' 64 bytes
+        uint4 *out = reinterpret_cast<uint4 *>(smem + kSmOut + (warp - kSoftWarp0) * 2048);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float x[32];
           tc::ld<32>(o_cols + 32 * q, x);
-          if (live) {
+          __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t b16[4];
+          for (int u = 0; u < 4; ++u) {
+            uint32_t b16[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * u + 2 * e] * inv, x[8 * u + 2 * e + 1] * inv);
-                b16[e] = *reinterpret_cast<const uint32_t *>(&b);
-              }
-              *reinterpret_cast<uint4 *>(c.out + at * (kD * 2) + q * 64 + u * 16) =
-                  make_uint4(b16[0], b16[1], b16[2], b16[3]);
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * u + 2 * e] * inv, x[8 * u + 2 * e + 1] * inv);
+              b16[e] = *reinterpret_cast<const uint32_t *>(&b);
             }
+            out[lane * 4 + (u ^ ((lane >> 1) & 3))] = make_uint4(b16[0], b16[1], b16[2], b16[3]);
+          }
+          __syncwarp();
+          uint4 y[4];
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int r = 8 * it + (lane >> 2);
+            y[it] = out[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+          }
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int64_t to = __shfl_sync(0xffffffffu, at, 8 * it + (lane >> 2));
+            if (to >= 0) *reinterpret_cast<uint4 *>(c.out + to * (kD * 2) + q * 64 + (lane & 3) * 16) = y[it];
           }
         }
         if (live && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;

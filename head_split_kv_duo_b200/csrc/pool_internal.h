@@ -59,7 +59,9 @@ constexpr int kPrefillMaxPages = kPrefillMaxTokens / kPoolTile + 2 * kPoolMaxSeq
 constexpr int kPrefillRows = 256;           // query rows of an item (two tensor-core tiles)
 constexpr int kPrefillCtas = 148;           // CTAs of the attention launch, one per SM
 constexpr int kPrefillParts = 2 * kPrefillCtas;  // pieces of cut items: a CTA's first and last
-constexpr int kPrefillRow = 132;            // floats of a partial row: 128 sums, max, sum of weights, 2 unused
+// floats of a partial row: 128 sums, max, sum of weights, 2 unused.  A piece is
+// [2 tiles][33 groups of four][128 rows][4]: the rows' threads write and read side by side.
+constexpr int kPrefillRow = 132;
 constexpr int kPrefillMaxRuns = 5;
 
 // Where an item's key tiles come from: the sequence's pages, its sinks and ring in slot

@@ -50,93 +50,90 @@ __device__ __forceinline__ int find(const int *first, int n, int x) {
   return lo;
 }
 
-// One warp per row of a cut item: weights of its pieces over the lanes, then four
-// dimensions a lane, eight pieces' loads in flight.
-__device__ __forceinline__ void join_row(const PoolFinishCall &c, int r, int lane) {
-  const PrefillCut &cut = c.cuts[r / kPrefillRows];
-  const int row = r % kPrefillRows, in = row % 128, segs = cut.pieces;
-  const int pos = cut.block * 2 * c.npos + row / 128 * c.npos + in / c.G;
-  if (in >= c.G * c.npos || pos >= c.n[cut.seq]) return;
-  auto part = [&](int seg) {
-    const int at = seg == 0 ? cut.part0 : cut.part1 + 2 * (seg - 1);
-    return c.partials + (static_cast<int64_t>(at) * kPrefillRows + row) * kPrefillRow;
+constexpr int kJoinBlocks = kPoolTile / 8;  // blocks of a cut item: eight dimensions of its 256 rows each
+
+// One thread per row: weights of its pieces, then eight dimensions of their sums, four
+// pieces' loads in flight.
+__device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
+  const PrefillCut &cut = c.cuts[block / kJoinBlocks];
+  const int group = block % kJoinBlocks * 2, tile = threadIdx.x / 128, row = threadIdx.x % 128, pieces = cut.pieces;
+  const int pos = (cut.block * 2 + tile) * c.npos + row / c.G;
+  if (row >= c.G * c.npos || pos >= c.n[cut.seq]) return;
+  auto part = [&](int i) {
+    const int at = i == 0 ? cut.part0 : cut.part1 + 2 * (i - 1);
+    return reinterpret_cast<const float4 *>(c.partials) + (at * 2 + tile) * (kPrefillRow / 4) * 128 + row;
   };
-  constexpr int kPer = (kPrefillCtas + 31) / 32;
-  float w[kPer], m = -INFINITY, l = 0.f;
-  float2 ml[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int seg = lane + 32 * i;
-    ml[i] = seg < segs ? *reinterpret_cast<const float2 *>(part(seg) + 128) : make_float2(-INFINITY, 0.f);
-    m = fmaxf(m, ml[i].x);
-  }
-  m = warp_max(m);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    // a piece that the row saw nothing of has no weight
-    w[i] = ml[i].x == -INFINITY ? 0.f : ex2(ml[i].x - m);
-    l = fmaf(ml[i].y, w[i], l);
-  }
-  l = warp_sum(l);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    for (int b = 0; b < 32 && 32 * i + b < segs; b += 8) {
-      float4 x[8];
-      float ws[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int seg = 32 * i + b + e;
-        ws[e] = __shfl_sync(0xffffffffu, w[i], b + e);
-        x[e] = seg < segs && ws[e] != 0.f ? *reinterpret_cast<const float4 *>(part(seg) + 4 * lane)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o.x = fmaf(ws[e], x[e].x, o.x);
-        o.y = fmaf(ws[e], x[e].y, o.y);
-        o.z = fmaf(ws[e], x[e].z, o.z);
-        o.w = fmaf(ws[e], x[e].w, o.w);
-      }
-    }
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) m = fmaxf(m, part(i)[32 * 128].x);
+  float o[8] = {};
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const float4 *p = part(i);
+    const float4 ml = p[32 * 128], a = p[group * 128], b = p[(group + 1) * 128];
+    const float w = ex2(ml.x - m);  // 0 for a piece that the row saw nothing of
+    l = fmaf(ml.y, w, l);
+    o[0] = fmaf(w, a.x, o[0]);
+    o[1] = fmaf(w, a.y, o[1]);
+    o[2] = fmaf(w, a.z, o[2]);
+    o[3] = fmaf(w, a.w, o[3]);
+    o[4] = fmaf(w, b.x, o[4]);
+    o[5] = fmaf(w, b.y, o[5]);
+    o[6] = fmaf(w, b.z, o[6]);
+    o[7] = fmaf(w, b.w, o[7]);
   }
   const float inv = 1.f / l;
-  const int64_t at = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + in % c.G;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2 *>(c.out + at * 256)[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-  if (lane == 0 && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
+  const int64_t at = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + row % c.G;
+  uint32_t b16[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+    b16[e] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  *reinterpret_cast<uint4 *>(c.out + at * 256 + group * 8) = make_uint4(b16[0], b16[1], b16[2], b16[3]);
+  if (group == 0 && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
 }
 
-// Warps: one per row of the cut items; then one per (token, KV head), K on the lower lanes, V on the
-// upper; then one per (sequence, retrieval head) for the rest of a page that the call
-// opened, and the block-table entries.
+// Blocks: those that join cut items; then warps, one per (eight tokens, KV head), K on the
+// lower lanes, V on the upper; then one per (sequence, retrieval head) for the rest of a
+// page that the call opened, and the block-table entries.
+constexpr int kAppendTokens = 8;
 __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_constant__ PoolFinishCall c) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (static_cast<int>(blockIdx.x) < c.ncuts * kJoinBlocks) return join_rows(c, blockIdx.x);
+  int64_t w = (static_cast<int64_t>(blockIdx.x - c.ncuts * kJoinBlocks) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const PoolLayerDesc &L = *c.layer;
-  const int64_t join_rows = static_cast<int64_t>(c.ncuts) * kPrefillRows;
-  if (w < join_rows) return join_row(c, static_cast<int>(w), lane);
-  w -= join_rows;
-  if (w < static_cast<int64_t>(c.tokens) * c.Hkv) {
-    const int t = static_cast<int>(w / c.Hkv), g = static_cast<int>(w % c.Hkv), idx = L.hm.kind_idx[g];
-    const int s = find(c.tok0, c.nseq, t), pos = c.len[s] + t - c.tok0[s], end = c.len[s] + c.n[s];
-    const bool is_k = lane < 16;
-    char *dst;
-    if (L.hm.is_retr[g]) {
-      const int page = c.pages[c.page0[s] + pos / kPoolTile - c.len[s] / kPoolTile];
-      dst = (is_k ? L.rk : L.rv) + ((static_cast<int64_t>(page) * L.Hr + idx) * kPoolTile + pos % kPoolTile) * 256;
-    } else {
-      if (pos >= c.S && pos < end - c.W) return;  // evicted within the call
-      const int slot = pos < c.S ? pos : c.S + pos % c.W;
-      dst = (is_k ? L.sk : L.sv) + ((static_cast<int64_t>(c.slot[s]) * L.Hs + idx) * (c.S + c.W) + slot) * 256;
+  const int64_t append = static_cast<int64_t>((c.tokens + kAppendTokens - 1) / kAppendTokens) * c.Hkv;
+  if (w < append) {
+    const int t0 = static_cast<int>(w / c.Hkv) * kAppendTokens, g = static_cast<int>(w % c.Hkv), idx = L.hm.kind_idx[g];
+    const bool is_k = lane < 16, retr = L.hm.is_retr[g];
+    const char *src = (is_k ? c.k : c.v) + (static_cast<int64_t>(t0) * c.Hkv + g) * 256 + (lane & 15) * 16;
+    char *base = retr ? (is_k ? L.rk : L.rv) : (is_k ? L.sk : L.sv);
+    uint4 x[kAppendTokens];
+#pragma unroll
+    for (int i = 0; i < kAppendTokens; ++i)
+      if (t0 + i < c.tokens) x[i] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(i) * c.Hkv * 256));
+    int s = find(c.tok0, c.nseq, t0);
+#pragma unroll
+    for (int i = 0; i < kAppendTokens; ++i) {
+      const int t = t0 + i;
+      if (t >= c.tokens) break;
+      while (t >= c.tok0[s + 1]) ++s;
+      const int pos = c.len[s] + t - c.tok0[s], end = c.len[s] + c.n[s];
+      int64_t row;
+      if (retr) {
+        const int page = c.pages[c.page0[s] + pos / kPoolTile - c.len[s] / kPoolTile];
+        row = (static_cast<int64_t>(page) * L.Hr + idx) * kPoolTile + pos % kPoolTile;
+      } else {
+        if (pos >= c.S && pos < end - c.W) continue;  // evicted within the call
+        row = (static_cast<int64_t>(c.slot[s]) * L.Hs + idx) * (c.S + c.W) + (pos < c.S ? pos : c.S + pos % c.W);
+      }
+      *reinterpret_cast<uint4 *>(base + row * 256 + (lane & 15) * 16) = x[i];
     }
-    const char *src = (is_k ? c.k : c.v) + w * 256;
-    reinterpret_cast<uint4 *>(dst)[lane & 15] = __ldg(reinterpret_cast<const uint4 *>(src) + (lane & 15));
     return;
   }
-  w -= static_cast<int64_t>(c.tokens) * c.Hkv;
+  w -= append;
   if (w < static_cast<int64_t>(c.nseq) * L.Hr) {
     const int s = static_cast<int>(w / L.Hr), h = static_cast<int>(w % L.Hr);
     const int end = c.len[s] + c.n[s], last = end / kPoolTile * kPoolTile;  // first row of the page that holds `end`
@@ -156,12 +153,16 @@ __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_c
   }
 }
 
-// Deals the items out, `tiles` key tiles each: whole ones in rounds, item r * ctas + c to
-// CTA c, as long as no CTA gets more than its even share, so that neighbours read the same
-// keys at about the same time; then the rest, cut where a CTA's share is full.  An item
-// costs a CTA about two tiles more than its tiles (queries, the first product, its rows'
-// way out, in pieces their way through the scratch); pieces of fewer than two tiles are
-// avoided, and a short call runs on as many CTAs as have four tiles each.
+// Deals the items out: whole ones in rounds, item r * ctas + c to CTA c, as long as no CTA
+// gets more than its even share of the cost, so that neighbours read the same keys at about
+// the same time; then the rest, cut where a CTA's share is full.  Costs are in quarters of a
+// retrieval head's key tile (2600 cycles): a streaming head's tile, masked for the most part, is
+// six, and a piece ten more than its tiles (queries, the first product, the rows' way out).
+// Pieces of fewer than two tiles are avoided, and a short call runs on as many CTAs as have
+// four tiles each.
+struct Item {
+  int tiles, tile_cost;
+};
 struct Deal {
   int whole = 0, ctas = 1;
   std::vector<PrefillShare> share;
@@ -170,22 +171,26 @@ struct Deal {
   };
   std::vector<Cut> cuts;
 };
-void deal_items(const std::vector<int> &tiles, int sms, Deal *d) {
-  constexpr int kItemCost = 2, kLeast = 2, kShareTiles = 4;
-  const int items = static_cast<int>(tiles.size());
-  int64_t total = 0;
-  for (int t : tiles) total += t;
-  d->ctas = static_cast<int>(std::min<int64_t>(std::min(sms, kPrefillCtas), std::max<int64_t>(1, total / kShareTiles)));
+constexpr int kTileCost = 4, kStreamingTileCost = 6, kPieceCost = 10;
+void deal_items(const std::vector<Item> &items, int sms, Deal *d) {
+  constexpr int kLeast = 2, kShareTiles = 4;
+  const int n = static_cast<int>(items.size());
+  auto cost = [&](int u) { return static_cast<int64_t>(items[u].tiles) * items[u].tile_cost + kPieceCost; };
+  int64_t tiles = 0, total = 0;
+  for (int u = 0; u < n; ++u) {
+    tiles += items[u].tiles;
+    total += cost(u);
+  }
+  d->ctas = static_cast<int>(std::min<int64_t>(std::min(sms, kPrefillCtas), std::max<int64_t>(1, tiles / kShareTiles)));
   const int ctas = d->ctas;
-  total += static_cast<int64_t>(items) * kItemCost;
   std::vector<int64_t> load(ctas);
   for (int64_t even = (total + ctas - 1) / ctas;;) {
     std::fill(load.begin(), load.end(), 0);
     int u = 0;
-    for (bool fits = true; fits && u + ctas <= items;) {
-      for (int c = 0; c < ctas; ++c) fits &= load[c] + tiles[u + c] + kItemCost <= even;
+    for (bool fits = true; fits && u + ctas <= n;) {
+      for (int c = 0; c < ctas; ++c) fits &= load[c] + cost(u + c) <= even;
       if (!fits) break;
-      for (int c = 0; c < ctas; ++c) load[c] += tiles[u + c] + kItemCost;
+      for (int c = 0; c < ctas; ++c) load[c] += cost(u + c);
       u += ctas;
     }
     d->whole = u;
@@ -193,30 +198,30 @@ void deal_items(const std::vector<int> &tiles, int sms, Deal *d) {
     d->cuts.clear();
     int rank = 0;
     int t0 = 0;  // tiles of item u already dealt
-    for (int c = 0; c < ctas && u < items; ++c) {
+    for (int c = 0; c < ctas && u < n; ++c) {
       int64_t room = even - load[c];
       PrefillShare &sh = d->share[c];
       sh = {u, t0, 0, 2 * rank};
-      while (u < items) {
-        const int rest = tiles[u] - t0;
-        const int64_t can = room - kItemCost;
+      while (u < n) {
+        const int rest = items[u].tiles - t0;
+        const int64_t can = (room - kPieceCost) / items[u].tile_cost;
         if (can < std::min(rest, kLeast)) break;
         int take = static_cast<int>(std::min<int64_t>(rest, can));
         if (rest - take < kLeast) take = rest;
         if (t0 > 0) ++d->cuts.back().pieces;
         else if (take < rest) d->cuts.push_back({u, 1, sh.item == u ? sh.part : sh.part + 1, 2 * (rank + 1)});
         sh.tiles += take;
-        room -= take + kItemCost;
+        room -= take * items[u].tile_cost + kPieceCost;
         t0 += take;
-        if (t0 < tiles[u]) break;
+        if (t0 < items[u].tiles) break;
         ++u;
         t0 = 0;
       }
       if (sh.tiles > 0) ++rank;
     }
-    if (u == items) return;
-    int64_t rest = -t0;
-    for (int i = u; i < items; ++i) rest += tiles[i] + kItemCost;
+    if (u == n) return;
+    int64_t rest = -static_cast<int64_t>(t0) * items[u].tile_cost;
+    for (int i = u; i < n; ++i) rest += cost(i);
     even += std::max<int64_t>(1, rest / ctas);
   }
 }
@@ -286,7 +291,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   }
   f.tok0[nseq] = tok;
   f.page0[nseq] = page;
-  std::vector<int> item_tiles;
+  std::vector<Item> items;
   for (int kind = 0; kind < 2; ++kind) {  // retrieval heads' items, then streaming heads'
     const int heads = kind == 0 ? Hr : Hs;
     int *first = kind == 0 ? a.rfirst : a.sfirst;
@@ -298,7 +303,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
         const int k = prefill_runs(kind == 0, f.len[s], n[s], b * 2 * f.npos, f.npos, P->S, P->W, runs);
         int t = 0;
         for (int r = 0; r < k; ++r) t += runs[r].count;
-        item_tiles.insert(item_tiles.end(), heads, t);
+        items.insert(items.end(), heads, Item{t, kind == 0 ? kTileCost : kStreamingTileCost});
       }
     }
   }
@@ -311,7 +316,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   }
   a.retr_items = a.rfirst[nseq];
   Deal deal;
-  deal_items(item_tiles, P->num_sms, &deal);
+  deal_items(items, P->num_sms, &deal);
   a.whole_items = deal.whole;
   a.ctas = deal.ctas;
   std::copy(deal.share.begin(), deal.share.end(), a.share);
@@ -342,9 +347,9 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   if (e == cudaSuccess)
     e = launch_via_hook([&] {
       const int64_t tail = std::max<int64_t>(static_cast<int64_t>(nseq) * Hr, (f.npages + 31) / 32);
-      const int64_t warps = static_cast<int64_t>(f.ncuts) * kPrefillRows + tokens * P->Hkv + tail;
+      const int64_t warps = (tokens + kAppendTokens - 1) / kAppendTokens * P->Hkv + tail;
       cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+      cfg.gridDim = dim3(static_cast<unsigned>(f.ncuts * kJoinBlocks + (warps + 7) / 8));
       cfg.blockDim = dim3(256);
       cfg.stream = st;
       cudaLaunchAttribute at{};  // its start overlaps the attention's end; it waits for it
