@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
   constexpr int LR = D / (2 * VE);                      // lanes of a row (two vectors each)
   constexpr int RW = 32 / LR;                           // rows of a group: one warp iteration
   constexpr int64_t kRow = D * static_cast<int64_t>(sizeof(T));
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float2 table[kNrThreads / 32][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t w = blockIdx.x * (kNrThreads / 32) + warp;
@@ -262,8 +264,7 @@ cudaError_t launch_norm_rope(NormRopeParams p, cudaStream_t st) {
   p.warps_per_token = (groups + p.iters - 1) / p.iters;
   const int64_t blocks = (p.n * p.warps_per_token + kNrThreads / 32 - 1) / (kNrThreads / 32);
   const auto kernel = p.interleaved ? norm_rope_kernel<T, D, true> : norm_rope_kernel<T, D, false>;
-  kernel<<<static_cast<unsigned>(blocks), kNrThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, blocks, kNrThreads, 0, st, p);
 }
 
 // Byte ranges of the call's tensors, for the overlap check.

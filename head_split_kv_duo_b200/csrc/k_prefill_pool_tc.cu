@@ -53,7 +53,8 @@ constexpr int kSmQ = 0, kSmK = kSmQ + kQT * kTile, kSmV = kSmK + kKStages * kTil
 constexpr int kSmMisc = kSmBar + 256;
 constexpr int kPieces = 4;  // pieces listed ahead
 constexpr int kSmOut = kSmMisc + 768;  // per softmax warp: 32 rows' 32 dims on their way out
-constexpr int kSmemAlloc = kSmOut + 4 * kQT * 2048 + 1024;  // slack for aligning the base to 1 KiB
+constexpr int kSmLists = kSmOut + 4 * kQT * 2048;
+constexpr int kSmemAlloc = kSmLists + static_cast<int>(sizeof(PrefillLists)) + 1024;  // slack for aligning the base to 1 KiB
 constexpr int kTmS = 0, kTmO = 256;
 constexpr int kPFirst = 96;  // keys of a tile whose P is handed over first
 
@@ -78,9 +79,10 @@ struct Tile {
 };
 
 // Item `u` of the call; its tiles go into `runs`.  Returns how many there are.
-__device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PoolLayerDesc &L, int u, Piece &w) {
+__device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PrefillLists &lists, const PoolLayerDesc &L, int u,
+                                       Piece &w) {
   w.retr = u < c.retr_items;
-  const int *first = w.retr ? c.rfirst : c.sfirst;
+  const int *first = w.retr ? lists.rfirst : lists.sfirst;
   const int v = w.retr ? u : u - c.retr_items;
   int lo = 0, hi = c.nseq - 1;  // the last sequence with first <= v
   while (lo < hi) {
@@ -88,10 +90,10 @@ __device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PoolLayer
     if (first[mid] <= v) lo = mid;
     else hi = mid - 1;
   }
-  w.len = c.len[lo];
-  w.n = c.n[lo];
-  w.slot = c.slot[lo];
-  w.tok0 = c.tok0[lo];
+  w.len = lists.len[lo];
+  w.n = lists.n[lo];
+  w.slot = lists.slot[lo];
+  w.tok0 = lists.tok0[lo];
   // heads fastest (neighbours in the grid read different heads' keys at the same places),
   // query blocks from the last -- the longest -- to the first
   const int npos = kBM / c.G, heads = w.retr ? c.Hr : c.Hs, rem = v - first[lo];
@@ -216,7 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PoolLayerDesc &L = *c.layer;
   const int npos = kBM / c.G;  // positions of a query tile
+  PrefillLists &lists = *reinterpret_cast<PrefillLists *>(smem + kSmLists);
 
+  // The prologue overlaps the end of the kernel before; what that may have written is read,
+  // and what it may read is written, behind the wait.  The lists are copied side by side:
+  // read one by one as parameters, each first touch would wait for the constant cache.
+  for (int i = tid; i < static_cast<int>(sizeof(PrefillLists) / 16); i += kThreads)
+    reinterpret_cast<uint4 *>(&lists)[i] = reinterpret_cast<const uint4 *>(&c.lists)[i];
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const bool softmax = i >= kBarPFull && i < kBarPFull + 2 * kQT, listed = i >= kBarPieceFree && i < kBarPieceFree + kPieces;
@@ -225,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
     fence_mbar_init();
     *abort_flag = 0;
   }
-  if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
   if (lane == 0 && (warp == 0 || warp == 2)) {
     // the layer's maps live in device memory, written before this launch
     const bool k = warp == 0;
@@ -236,6 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
     if (k) tc::prefetch_map(&c.tm_q);
     tc::prefetch_map(k ? &c.tm_k : &c.tm_v);
   }
+  // (tensor memory is taken behind the wait as well: a kernel before may still want some)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         mbar_arrive(bar(kBarPiece + p % kPieces));
         ++p;
       };
-      const PrefillShare sh = c.share[blockIdx.x];
+      const PrefillShare sh = lists.share[blockIdx.x];
       int u = blockIdx.x, j0 = 0, left = sh.tiles;
       while (ok) {
         const bool whole = u < c.whole_items;
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         if (!whole && left == 0) break;
         Piece *w = slot();
         if (!ok) break;
-        const int tiles = item_of(c, L, u, *w), nt = whole ? tiles : min(tiles - j0, left);
+        const int tiles = item_of(c, lists, L, u, *w), nt = whole ? tiles : min(tiles - j0, left);
         w->j0 = j0;
         w->nt = nt;
         w->part = nt == tiles ? -1 : (u == sh.item ? sh.part : sh.part + 1);
@@ -664,8 +674,7 @@ cudaError_t prepare_prefill_pool_tc(PoolPrefillCall *c, const void *q, const voi
 }
 
 cudaError_t launch_prefill_pool_tc(const PoolPrefillCall &c, cudaStream_t st) {
-  prefill_pool_kernel<<<c.ctas, kThreads, kSmemAlloc, st>>>(c);
-  return cudaGetLastError();
+  return launch_overlapped(prefill_pool_kernel, c.ctas, kThreads, kSmemAlloc, st, c);
 }
 
 }  // namespace duo

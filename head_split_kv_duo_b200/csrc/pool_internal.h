@@ -128,6 +128,13 @@ struct PrefillShare {
 // The attention launch.  Sequences are listed by decreasing work per item; retrieval heads'
 // items come first.  CTA c works on items c, c + grid, ... below whole_items, then on its
 // share of the others.
+struct alignas(16) PrefillLists {
+  int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
+  int tok0[kPoolMaxSeqs];        // first of the sequence's tokens in the call's tensors
+  int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // items before a sequence, per kind
+  int unused[2];
+  PrefillShare share[kPrefillCtas];
+};
 struct PoolPrefillCall {
   CUtensorMap tm_q, tm_k, tm_v;  // q [tokens][Hq][d], k and v [tokens][Hkv][d]
   const PoolLayerDesc *layer;    // device
@@ -139,10 +146,7 @@ struct PoolPrefillCall {
   uint32_t *status;
   int nseq, Hq, Hkv, G, S, W, Hr, Hs, retr_items, whole_items, ctas;
   float scale_log2;
-  int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
-  int tok0[kPoolMaxSeqs];        // first of the sequence's tokens in the call's tensors
-  int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // items before a sequence, per kind
-  PrefillShare share[kPrefillCtas];
+  PrefillLists lists;
 };
 // Positions per query tile and items (of two tiles) that cover n positions of one KV head.
 inline int prefill_tile_positions(int G) { return 128 / G; }

@@ -63,24 +63,40 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
     const int at = i == 0 ? cut.part0 : cut.part1 + 2 * (i - 1);
     return reinterpret_cast<const float4 *>(c.partials) + (at * 2 + tile) * (kPrefillRow / 4) * 128 + row;
   };
-  float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) m = fmaxf(m, part(i)[32 * 128].x);
-  float o[8] = {};
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
-    const float4 *p = part(i);
-    const float4 ml = p[32 * 128], a = p[group * 128], b = p[(group + 1) * 128];
-    const float w = ex2(ml.x - m);  // 0 for a piece that the row saw nothing of
-    l = fmaf(ml.y, w, l);
-    o[0] = fmaf(w, a.x, o[0]);
-    o[1] = fmaf(w, a.y, o[1]);
-    o[2] = fmaf(w, a.z, o[2]);
-    o[3] = fmaf(w, a.w, o[3]);
-    o[4] = fmaf(w, b.x, o[4]);
-    o[5] = fmaf(w, b.y, o[5]);
-    o[6] = fmaf(w, b.z, o[6]);
-    o[7] = fmaf(w, b.w, o[7]);
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  for (int i0 = 0; i0 < pieces; i0 += 4) {
+    float4 ml[4], x[4], y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ml[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      x[e] = y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + e < pieces) {
+        const float4 *p = part(i0 + e);
+        ml[e] = p[32 * 128];
+        x[e] = p[group * 128];
+        y[e] = p[(group + 1) * 128];
+      }
+    }
+    const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+    if (top == -INFINITY) continue;  // the row saw nothing so far
+    const float old = ex2(m - top);  // 0 while m is -inf
+    m = top;
+    l *= old;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] *= old;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = ex2(ml[e].x - m);
+      l = fmaf(ml[e].y, w, l);
+      o[0] = fmaf(w, x[e].x, o[0]);
+      o[1] = fmaf(w, x[e].y, o[1]);
+      o[2] = fmaf(w, x[e].z, o[2]);
+      o[3] = fmaf(w, x[e].w, o[3]);
+      o[4] = fmaf(w, y[e].x, o[4]);
+      o[5] = fmaf(w, y[e].y, o[5]);
+      o[6] = fmaf(w, y[e].z, o[6]);
+      o[7] = fmaf(w, y[e].w, o[7]);
+    }
   }
   const float inv = 1.f / l;
   const int64_t at = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + row % c.G;
@@ -156,10 +172,11 @@ __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_c
 // Deals the items out: whole ones in rounds, item r * ctas + c to CTA c, as long as no CTA
 // gets more than its even share of the cost, so that neighbours read the same keys at about
 // the same time; then the rest, cut where a CTA's share is full.  Costs are in quarters of a
-// retrieval head's key tile (2600 cycles): a streaming head's tile, masked for the most part, is
-// six, and a piece ten more than its tiles (queries, the first product, the rows' way out).
+// retrieval head's key tile (2650 cycles): a streaming head's tile, masked for the most part,
+// is five, and a piece twelve more than its tiles (queries, the first product, masks at
+// its ends, the rows' way out).
 // Pieces of fewer than two tiles are avoided, and a short call runs on as many CTAs as have
-// four tiles each.
+// two tiles each.
 struct Item {
   int tiles, tile_cost;
 };
@@ -171,9 +188,9 @@ struct Deal {
   };
   std::vector<Cut> cuts;
 };
-constexpr int kTileCost = 4, kStreamingTileCost = 6, kPieceCost = 10;
+constexpr int kTileCost = 4, kStreamingTileCost = 5, kPieceCost = 12;
 void deal_items(const std::vector<Item> &items, int sms, Deal *d) {
-  constexpr int kLeast = 2, kShareTiles = 4;
+  constexpr int kLeast = 2, kShareTiles = 2;
   const int n = static_cast<int>(items.size());
   auto cost = [&](int u) { return static_cast<int64_t>(items[u].tiles) * items[u].tile_cost + kPieceCost; };
   int64_t tiles = 0, total = 0;
@@ -294,7 +311,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   std::vector<Item> items;
   for (int kind = 0; kind < 2; ++kind) {  // retrieval heads' items, then streaming heads'
     const int heads = kind == 0 ? Hr : Hs;
-    int *first = kind == 0 ? a.rfirst : a.sfirst;
+    int *first = kind == 0 ? a.lists.rfirst : a.lists.sfirst;
     for (int i = 0; i < nseq; ++i) {
       const int s = order[i], blocks = prefill_blocks(n[s], P->G);
       first[i + 1] = first[i] + blocks * heads;
@@ -309,23 +326,23 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   }
   for (int i = 0; i < nseq; ++i) {
     const int s = order[i];
-    a.slot[i] = f.slot[s];
-    a.len[i] = f.len[s];
-    a.n[i] = f.n[s];
-    a.tok0[i] = f.tok0[s];
+    a.lists.slot[i] = f.slot[s];
+    a.lists.len[i] = f.len[s];
+    a.lists.n[i] = f.n[s];
+    a.lists.tok0[i] = f.tok0[s];
   }
-  a.retr_items = a.rfirst[nseq];
+  a.retr_items = a.lists.rfirst[nseq];
   Deal deal;
   deal_items(items, P->num_sms, &deal);
   a.whole_items = deal.whole;
   a.ctas = deal.ctas;
-  std::copy(deal.share.begin(), deal.share.end(), a.share);
+  std::copy(deal.share.begin(), deal.share.end(), a.lists.share);
   f.ncuts = static_cast<int>(deal.cuts.size());
   for (int i = 0; i < f.ncuts; ++i) {
     const Deal::Cut &cut = deal.cuts[i];
     const bool retr = cut.item < a.retr_items;
     const int u = retr ? cut.item : cut.item - a.retr_items, heads = retr ? Hr : Hs;
-    const int *first = retr ? a.rfirst : a.sfirst;
+    const int *first = retr ? a.lists.rfirst : a.lists.sfirst;
     const int at = static_cast<int>(std::upper_bound(first, first + nseq, u) - first) - 1;
     const HeadMap &hm = P->h_layers[layer].hm;
     const int rem = u - first[at];
@@ -348,16 +365,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     e = launch_via_hook([&] {
       const int64_t tail = std::max<int64_t>(static_cast<int64_t>(nseq) * Hr, (f.npages + 31) / 32);
       const int64_t warps = (tokens + kAppendTokens - 1) / kAppendTokens * P->Hkv + tail;
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(static_cast<unsigned>(f.ncuts * kJoinBlocks + (warps + 7) / 8));
-      cfg.blockDim = dim3(256);
-      cfg.stream = st;
-      cudaLaunchAttribute at{};  // its start overlaps the attention's end; it waits for it
-      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      at.val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = &at;
-      cfg.numAttrs = 1;
-      return cudaLaunchKernelEx(&cfg, pool_prefill_finish_kernel, f);
+      return launch_overlapped(pool_prefill_finish_kernel, f.ncuts * kJoinBlocks + (warps + 7) / 8, 256, 0, st, f);
     });
   if (e != cudaSuccess) {  // the cache is written by the last launch alone
     for (int i = nseq - 1; i >= 0; --i) {

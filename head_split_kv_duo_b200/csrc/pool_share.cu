@@ -58,6 +58,8 @@ __device__ __forceinline__ void copy_piece(const char *src, int rows, int valid,
 }
 
 __global__ void __launch_bounds__(256) pool_share_kernel(const __grid_constant__ PoolShareCall c) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const unsigned piece = blockIdx.x % c.pieces, h = blockIdx.x / c.pieces;
   const int g = h % c.Hkv, kv = (h / c.Hkv) & 1, layer = h / c.heads2;
   const PoolLayerDesc &A = c.src_layers[layer], &B = c.dst_layers[layer];
@@ -151,8 +153,7 @@ duo_status share_sequence(const duo_pool *P, int seq, duo_pool *Q, int shared, i
     c.pieces = std::max(c.pieces, 1);
     const int64_t blocks = static_cast<int64_t>(P->layers) * c.heads2 * c.pieces;
     e = blocks > INT32_MAX ? cudaErrorInvalidValue : launch_via_hook([&] {
-      pool_share_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(c);
-      return cudaGetLastError();
+      return launch_overlapped(pool_share_kernel, blocks, 256, 0, st, c);
     });
     done += c.npages;
   } while (e == cudaSuccess && done < copied);
