@@ -79,8 +79,7 @@ struct Tile {
 };
 
 // Item `u` of the call; its tiles go into `runs`.  Returns how many there are.
-__device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PrefillLists &lists, const PoolLayerDesc &L, int u,
-                                       Piece &w) {
+__device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PrefillLists &lists, int u, Piece &w) {
   w.retr = u < c.retr_items;
   const int *first = w.retr ? lists.rfirst : lists.sfirst;
   const int v = w.retr ? u : u - c.retr_items;
@@ -99,7 +98,7 @@ __device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PrefillLi
   const int npos = kBM / c.G, heads = w.retr ? c.Hr : c.Hs, rem = v - first[lo];
   const int ntq = (w.n + npos - 1) / npos, blocks = (ntq + kQT - 1) / kQT, qb = blocks - 1 - rem / heads;
   w.idx = rem % heads;
-  w.g = w.retr ? L.hm.retr_head[w.idx] : L.hm.strm_head[w.idx];
+  w.g = w.retr ? lists.retr_head[w.idx] : lists.strm_head[w.idx];
   w.r0 = qb * kQT * npos;
   w.nq = min(kQT, ntq - qb * kQT);
   const int k = prefill_runs(w.retr, w.len, w.n, w.r0, npos, c.S, c.W, w.runs);
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         if (!whole && left == 0) break;
         Piece *w = slot();
         if (!ok) break;
-        const int tiles = item_of(c, lists, L, u, *w), nt = whole ? tiles : min(tiles - j0, left);
+        const int tiles = item_of(c, lists, u, *w), nt = whole ? tiles : min(tiles - j0, left);
         w->j0 = j0;
         w->nt = nt;
         w->part = nt == tiles ? -1 : (u == sh.item ? sh.part : sh.part + 1);

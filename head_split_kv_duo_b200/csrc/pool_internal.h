@@ -133,6 +133,7 @@ struct alignas(16) PrefillLists {
   int tok0[kPoolMaxSeqs];        // first of the sequence's tokens in the call's tensors
   int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // items before a sequence, per kind
   int unused[2];
+  uint8_t retr_head[kMaxKvHeads], strm_head[kMaxKvHeads];  // KV heads of each kind
   PrefillShare share[kPrefillCtas];
 };
 struct PoolPrefillCall {

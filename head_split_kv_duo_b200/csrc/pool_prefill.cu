@@ -20,6 +20,7 @@ namespace {
 // in the scratch, part0, part1, part1 + 2, ...
 struct PrefillCut {
   int seq, block, head, pieces, part0, part1;
+  int join0;  // blocks of the last launch that join cuts before it
 };
 
 // The call's last launch, sequences in the caller's order.
@@ -31,7 +32,7 @@ struct PoolFinishCall {
   char *out;
   float *lse;
   const float *partials;
-  int nseq, tokens, Hq, Hkv, G, S, W, npos, npages, ncuts;
+  int nseq, tokens, Hq, Hkv, G, S, W, npos, npages, ncuts, join_blocks;
   int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
   int tok0[kPoolMaxSeqs + 1];
   int page0[kPoolMaxSeqs + 1];  // a sequence's entries in `pages`, from logical page len / 128 on
@@ -50,28 +51,39 @@ __device__ __forceinline__ int find(const int *first, int n, int x) {
   return lo;
 }
 
-constexpr int kJoinBlocks = kPoolTile / 8;  // blocks of a cut item: eight dimensions of its 256 rows each
-
-// One thread per row: weights of its pieces, then eight dimensions of their sums, four
-// pieces' loads in flight.
+// A block joins eight dimensions of a cut item's 256 rows, one thread per row, four pieces'
+// loads in flight; or, of more than four pieces, of 64 of its rows, four threads per row,
+// each joining every fourth piece, and the first of them the four.
+constexpr int kJoinGroups = 128 / 8;
+__host__ __device__ inline int join_threads(int pieces) { return pieces > 4 ? 4 : 1; }
 __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
-  const PrefillCut &cut = c.cuts[block / kJoinBlocks];
-  const int group = block % kJoinBlocks * 2, tile = threadIdx.x / 128, row = threadIdx.x % 128, pieces = cut.pieces;
+  __shared__ float others[3][10][64];
+  int at = 0;  // the last cut with join0 <= block
+  for (int hi = c.ncuts - 1; at < hi;) {
+    const int mid = (at + hi + 1) >> 1;
+    if (c.cuts[mid].join0 <= block) at = mid;
+    else hi = mid - 1;
+  }
+  const PrefillCut &cut = c.cuts[at];
+  const int pieces = cut.pieces, threads = join_threads(pieces), rows = kPrefillRows / threads;
+  const int local = block - cut.join0, group = local % kJoinGroups * 2, thread = threadIdx.x / rows;
+  const int r = local / kJoinGroups * rows + threadIdx.x % rows, tile = r / 128, row = r % 128;
   const int pos = (cut.block * 2 + tile) * c.npos + row / c.G;
-  if (row >= c.G * c.npos || pos >= c.n[cut.seq]) return;
+  const bool live = row < c.G * c.npos && pos < c.n[cut.seq];
+  if (threads == 1 && !live) return;
   auto part = [&](int i) {
-    const int at = i == 0 ? cut.part0 : cut.part1 + 2 * (i - 1);
-    return reinterpret_cast<const float4 *>(c.partials) + (at * 2 + tile) * (kPrefillRow / 4) * 128 + row;
+    const int place = i == 0 ? cut.part0 : cut.part1 + 2 * (i - 1);
+    return reinterpret_cast<const float4 *>(c.partials) + (place * 2 + tile) * (kPrefillRow / 4) * 128 + row;
   };
   float m = -INFINITY, l = 0.f, o[8] = {};
-  for (int i0 = 0; i0 < pieces; i0 += 4) {
+  for (int i0 = thread; i0 < pieces && live; i0 += 4 * threads) {
     float4 ml[4], x[4], y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       ml[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       x[e] = y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + e < pieces) {
-        const float4 *p = part(i0 + e);
+      if (i0 + e * threads < pieces) {
+        const float4 *p = part(i0 + e * threads);
         ml[e] = p[32 * 128];
         x[e] = p[group * 128];
         y[e] = p[(group + 1) * 128];
@@ -98,16 +110,39 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
       o[7] = fmaf(w, y[e].w, o[7]);
     }
   }
+  if (threads > 1) {
+    const int i = threadIdx.x % 64;
+    if (thread > 0) {
+      float *to = &others[thread - 1][0][i];
+      to[0] = m;
+      to[64] = l;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) to[64 * (2 + k)] = o[k];
+    }
+    __syncthreads();
+    if (thread > 0 || !live) return;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const float *from = &others[t][0][i];
+      const float top = fmaxf(m, from[0]);
+      if (top == -INFINITY) continue;
+      const float a = ex2(m - top), b = ex2(from[0] - top);
+      m = top;
+      l = l * a + from[64] * b;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = o[k] * a + from[64 * (2 + k)] * b;
+    }
+  }
   const float inv = 1.f / l;
-  const int64_t at = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + row % c.G;
+  const int64_t out = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + row % c.G;
   uint32_t b16[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
     b16[e] = *reinterpret_cast<const uint32_t *>(&b);
   }
-  *reinterpret_cast<uint4 *>(c.out + at * 256 + group * 8) = make_uint4(b16[0], b16[1], b16[2], b16[3]);
-  if (group == 0 && c.lse) c.lse[at] = (m + lg2(l)) * kLn2;
+  *reinterpret_cast<uint4 *>(c.out + out * 256 + group * 8) = make_uint4(b16[0], b16[1], b16[2], b16[3]);
+  if (group == 0 && c.lse) c.lse[out] = (m + lg2(l)) * kLn2;
 }
 
 // Blocks: those that join cut items; then warps, one per (eight tokens, KV head), K on the
@@ -116,8 +151,8 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
 constexpr int kAppendTokens = 8;
 __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_constant__ PoolFinishCall c) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) < c.ncuts * kJoinBlocks) return join_rows(c, blockIdx.x);
-  int64_t w = (static_cast<int64_t>(blockIdx.x - c.ncuts * kJoinBlocks) * blockDim.x + threadIdx.x) >> 5;
+  if (static_cast<int>(blockIdx.x) < c.join_blocks) return join_rows(c, blockIdx.x);
+  int64_t w = (static_cast<int64_t>(blockIdx.x - c.join_blocks) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const PoolLayerDesc &L = *c.layer;
   const int64_t append = static_cast<int64_t>((c.tokens + kAppendTokens - 1) / kAppendTokens) * c.Hkv;
@@ -331,6 +366,9 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     a.lists.n[i] = f.n[s];
     a.lists.tok0[i] = f.tok0[s];
   }
+  const HeadMap &hm = P->h_layers[layer].hm;
+  std::copy(hm.retr_head, hm.retr_head + Hr, a.lists.retr_head);
+  std::copy(hm.strm_head, hm.strm_head + Hs, a.lists.strm_head);
   a.retr_items = a.lists.rfirst[nseq];
   Deal deal;
   deal_items(items, P->num_sms, &deal);
@@ -344,10 +382,10 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     const int u = retr ? cut.item : cut.item - a.retr_items, heads = retr ? Hr : Hs;
     const int *first = retr ? a.lists.rfirst : a.lists.sfirst;
     const int at = static_cast<int>(std::upper_bound(first, first + nseq, u) - first) - 1;
-    const HeadMap &hm = P->h_layers[layer].hm;
     const int rem = u - first[at];
     f.cuts[i] = {order[at], prefill_blocks(n[order[at]], P->G) - 1 - rem / heads,
-                 retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1};
+                 retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1, f.join_blocks};
+    f.join_blocks += kJoinGroups * join_threads(cut.pieces);
   }
   if (!dry_run() && prepare_prefill_pool_tc(&a, q, k, v, f.tokens) != cudaSuccess) return DUO_ERR_CUDA;
   for (int i = 0; i < nseq; ++i) P->pages[seqs[i]].reserve(static_cast<size_t>(need[i]));
@@ -365,7 +403,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     e = launch_via_hook([&] {
       const int64_t tail = std::max<int64_t>(static_cast<int64_t>(nseq) * Hr, (f.npages + 31) / 32);
       const int64_t warps = (tokens + kAppendTokens - 1) / kAppendTokens * P->Hkv + tail;
-      return launch_overlapped(pool_prefill_finish_kernel, f.ncuts * kJoinBlocks + (warps + 7) / 8, 256, 0, st, f);
+      return launch_overlapped(pool_prefill_finish_kernel, f.join_blocks + (warps + 7) / 8, 256, 0, st, f);
     });
   if (e != cudaSuccess) {  // the cache is written by the last launch alone
     for (int i = nseq - 1; i >= 0; --i) {

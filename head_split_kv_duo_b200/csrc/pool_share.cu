@@ -7,10 +7,10 @@
 // and rings of streaming heads are overwritten in place by appends, so each child gets
 // its own.  A copy into another pool shares nothing.
 //
-// Both are one kernel: 32 KiB pieces (128 rows of one head of K or V) of the source's
+// Both are one kernel: pieces (32 or 64 rows of one head of K or V) of the source's
 // pages and rings, read once and written to every destination; rows past the source's
 // length are written as zeros without being read.  A piece is one block of 256 threads
-// with eight 16-byte loads each in flight, so a fork of one child is a single wave of
+// with two or four 16-byte loads each in flight, so a fork of one child is a single wave of
 // loads over the GPU, and many pieces stream at the copy bandwidth of HBM.
 #include "device_common.cuh"
 #include "nvtx_range.h"
@@ -39,25 +39,28 @@ struct PoolShareCall {
 
 // rows [0, valid) of a piece of `rows` rows, read once, into the same place of every
 // destination; the others as zeros
-template <class Dst>
+template <int kShareRows, class Dst>
 __device__ __forceinline__ void copy_piece(const char *src, int rows, int valid, int ndst, Dst dst) {
-  uint4 x[8];
+  constexpr int kShareLoads = kShareRows * 16 / 256;  // 16-byte vectors of a thread
+  uint4 x[kShareLoads];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < kShareLoads; ++j) {
     const int i = threadIdx.x + 256 * j;  // 16 vectors a row
     x[j] = i < valid * 16 ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
   }
   for (int c = 0; c < ndst; ++c) {
     uint4 *d = reinterpret_cast<uint4 *>(dst(c));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kShareLoads; ++j) {
       const int i = threadIdx.x + 256 * j;
       if (i < rows * 16) d[i] = x[j];
     }
   }
 }
 
+template <int kShareRows>
 __global__ void __launch_bounds__(256) pool_share_kernel(const __grid_constant__ PoolShareCall c) {
+  constexpr int kSharePage = kPoolTile / kShareRows;  // pieces of a page
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const unsigned piece = blockIdx.x % c.pieces, h = blockIdx.x / c.pieces;
@@ -65,22 +68,24 @@ __global__ void __launch_bounds__(256) pool_share_kernel(const __grid_constant__
   const PoolLayerDesc &A = c.src_layers[layer], &B = c.dst_layers[layer];
   const int idx = A.hm.kind_idx[g];
   if (A.hm.is_retr[g]) {
-    if (static_cast<int>(piece) < c.npages) {
-      const int64_t at = static_cast<int64_t>(c.page0 + piece) * kPoolTile;
-      const int valid = static_cast<int>(c.len - at < kPoolTile ? c.len - at : kPoolTile);
-      const char *src = (kv ? A.rv : A.rk) + (static_cast<int64_t>(c.list[piece]) * A.Hr + idx) * kPoolTile * 256;
+    const int page = piece / kSharePage, row0 = piece % kSharePage * kShareRows;
+    if (page < c.npages) {
+      const int64_t left = c.len - static_cast<int64_t>(c.page0 + page) * kPoolTile - row0;
+      const int valid = static_cast<int>(left < 0 ? 0 : left < kShareRows ? left : kShareRows);
+      const char *src = (kv ? A.rv : A.rk) + ((static_cast<int64_t>(c.list[page]) * A.Hr + idx) * kPoolTile + row0) * 256;
       char *base = kv ? B.rv : B.rk;
-      const int *to = c.list + c.npages + piece * c.ndst;
-      copy_piece(src, kPoolTile, valid, c.ndst,
-                 [&](int d) { return base + (static_cast<int64_t>(to[d]) * B.Hr + idx) * kPoolTile * 256; });
+      const int *to = c.list + c.npages + page * c.ndst;
+      copy_piece<kShareRows>(src, kShareRows, valid, c.ndst, [&](int d) {
+        return base + ((static_cast<int64_t>(to[d]) * B.Hr + idx) * kPoolTile + row0) * 256;
+      });
     }
   } else if (c.ring_rows >= 0) {
-    const int slots = c.S + c.W, row0 = static_cast<int>(piece) * kPoolTile;
+    const int slots = c.S + c.W, row0 = static_cast<int>(piece) * kShareRows;
     if (row0 < slots) {
-      const int rows = min(kPoolTile, slots - row0), valid = max(0, min(rows, c.ring_rows - row0));
+      const int rows = min(kShareRows, slots - row0), valid = max(0, min(rows, c.ring_rows - row0));
       const char *src = (kv ? A.sv : A.sk) + ((static_cast<int64_t>(c.src_slot) * A.Hs + idx) * slots + row0) * 256;
       char *base = kv ? B.sv : B.sk;
-      copy_piece(src, rows, valid, c.ndst, [&](int d) {
+      copy_piece<kShareRows>(src, rows, valid, c.ndst, [&](int d) {
         return base + ((static_cast<int64_t>(c.dst_slot[d]) * B.Hs + idx) * slots + row0) * 256;
       });
     }
@@ -149,11 +154,18 @@ duo_status share_sequence(const duo_pool *P, int seq, duo_pool *Q, int shared, i
       c.list[i] = src[c.page0 + i];
       for (int d = 0; d < n; ++d) c.list[c.npages + i * n + d] = lists[d][c.page0 + i];
     }
-    c.pieces = std::max(c.npages, c.ring_rows >= 0 ? (P->S + P->W + kPoolTile - 1) / kPoolTile : 1);
-    c.pieces = std::max(c.pieces, 1);
-    const int64_t blocks = static_cast<int64_t>(P->layers) * c.heads2 * c.pieces;
-    e = blocks > INT32_MAX ? cudaErrorInvalidValue : launch_via_hook([&] {
-      return launch_overlapped(pool_share_kernel, blocks, 256, 0, st, c);
+    auto blocks = [&](int rows) {
+      c.pieces = std::max(std::max(c.npages * (kPoolTile / rows), c.ring_rows >= 0 ? (P->S + P->W + rows - 1) / rows : 1), 1);
+      return static_cast<int64_t>(P->layers) * c.heads2 * c.pieces;
+    };
+    // 64 rows a piece stream best (32900 tokens of 8 layers 170 us, 197 with 32); where that
+    // is less than twice what the GPU holds at once, pieces of 32 share the work more
+    // evenly (eight children of 4200 tokens 22.5 us for 24.6)
+    constexpr int64_t kFew = 2 * 8 * 148;
+    const bool few = blocks(64) < kFew;
+    const int64_t grid = blocks(few ? 32 : 64);
+    e = grid > INT32_MAX ? cudaErrorInvalidValue : launch_via_hook([&] {
+      return launch_overlapped(few ? pool_share_kernel<32> : pool_share_kernel<64>, grid, 256, 0, st, c);
     });
     done += c.npages;
   } while (e == cudaSuccess && done < copied);
