@@ -261,6 +261,12 @@ cudaError_t launch_pool_chunk_append(const PoolChunkAppend &c, int Hr, int Hs, c
 // decode tiling shared by host (split sizing) and device
 int decode_tokens_per_stage(duo_dtype dt, int D, bool int4);
 
+// A byte range of a call's tensors, for its overlap check.
+struct Span {
+  uintptr_t lo, hi;
+  bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
+};
+
 // A launch whose start may overlap the end of the kernel before it in the stream: the
 // kernel executes griddepcontrol.wait before it reads or writes global memory.
 template <class Param>

@@ -267,12 +267,6 @@ cudaError_t launch_norm_rope(NormRopeParams p, cudaStream_t st) {
   return launch_overlapped(kernel, blocks, kNrThreads, 0, st, p);
 }
 
-// Byte ranges of the call's tensors, for the overlap check.
-struct Span {
-  uintptr_t lo, hi;
-  bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
-};
-
 }  // namespace
 
 }  // namespace duo

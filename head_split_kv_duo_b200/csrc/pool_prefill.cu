@@ -289,6 +289,15 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     tokens += n[i];
   }
   if (tokens > kPrefillMaxTokens) return DUO_ERR_INVALID;
+  {  // the results overlap neither the inputs, nor one another, nor the pool
+    auto span = [&](const void *p, int64_t bytes) { return Span{reinterpret_cast<uintptr_t>(p),
+                                                                reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(p ? bytes : 0)}; };
+    const int64_t qb = tokens * P->Hq * 256, kb = tokens * P->Hkv * 256;
+    const Span o = span(out, qb), l = span(lse, tokens * P->Hq * 4);
+    if (o.meets(l)) return DUO_ERR_INVALID;
+    for (const Span &x : {span(q, qb), span(k, kb), span(v, kb), span(P->buf, static_cast<int64_t>(P->bytes))})
+      if (x.meets(o) || x.meets(l)) return DUO_ERR_INVALID;
+  }
   std::vector<int64_t> need(nseq), tiles(nseq);
   const int Hr = P->hr[layer], Hs = P->hs[layer];
   for (int i = 0; i < nseq; ++i) {

@@ -489,6 +489,7 @@ class DuoPool:
         if nbytes == 0:
             raise DuoError(DUO_ERR_INVALID, "duo_pool_bytes")
         self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        self._index = self.buffer.device.index if self.buffer.device.type == "cuda" else None
         base = (self.buffer.data_ptr() + 255) // 256 * 256
         st, self.handle = duo_pool_create(layers, kv_heads, 128, self.mask, S, W, max_seqs, max_len, num_pages,
                                           self.opts, base, nbytes)
@@ -512,9 +513,11 @@ class DuoPool:
 
     def _stream(self, stream):
         """The launch stream: `stream`, or the current one of the pool's device, which must be the current device."""
-        dev = self.buffer.device
-        if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-            raise ValueError(f"the pool is on {dev}, which is not the current device")
+        if self._index is not None:
+            if self._index != torch.cuda.current_device():
+                raise ValueError(f"the pool is on cuda:{self._index}, which is not the current device")
+            if stream is None:
+                return torch._C._cuda_getCurrentRawStream(self._index)
         return _stream_ptr(stream)
 
     def open(self, stream=None) -> int:
@@ -557,25 +560,30 @@ class DuoPool:
                     "duo_pool_decode_step")
         return out, lse
 
+    def _rows(self, t, name, tokens, heads, device):
+        if t.dtype != torch.bfloat16 or t.shape != (tokens, heads, 128) or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name}: expected contiguous bf16 [{tokens}][{heads}][128] on {device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+
     def prefill(self, layer, seqs, n, q, k, v, out=None, lse=None, want_lse=True, stream=None):
         """duo_pool_prefill: the n[i] tokens of each listed sequence attend and are appended; q, out
         [sum n][Hq][128], k, v [sum n][Hkv][128] bf16, sequence after sequence -> (out, lse)."""
         if len(n) != len(seqs):
             raise ValueError(f"n: expected {len(seqs)} lengths, got {len(n)}")
         tokens, dev = sum(n), self.buffer.device
-        shapes = (tokens, self.q_heads, 128), (tokens, self.kv_heads, 128)
-        for t, name, shape in ((q, "q", shapes[0]), (k, "k", shapes[1]), (v, "v", shapes[1]), (out, "out", shapes[0])):
-            if t is not None and (t.dtype != torch.bfloat16 or t.shape != shape or not t.is_contiguous() or
-                                  t.device != dev):
-                raise ValueError(f"{name}: expected contiguous bf16 {list(shape)} on {dev}, got {t.dtype} "
-                                 f"{tuple(t.shape)} on {t.device}")
+        self._rows(q, "q", tokens, self.q_heads, dev)
+        self._rows(k, "k", tokens, self.kv_heads, dev)
+        self._rows(v, "v", tokens, self.kv_heads, dev)
         if out is None:
             out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty(shapes[0][:2], dtype=torch.float32, device=dev)
-        elif lse is not None and (lse.dtype != torch.float32 or lse.shape != shapes[0][:2] or
-                                  not lse.is_contiguous() or lse.device != dev):
-            raise ValueError(f"lse: expected contiguous fp32 {list(shapes[0][:2])} on {dev}")
+        else:
+            self._rows(out, "out", tokens, self.q_heads, dev)
+        if lse is None:
+            if want_lse:
+                lse = q.new_empty((tokens, self.q_heads), dtype=torch.float32)
+        elif lse.dtype != torch.float32 or lse.shape != (tokens, self.q_heads) or not lse.is_contiguous() or \
+                lse.device != dev:
+            raise ValueError(f"lse: expected contiguous fp32 [{tokens}][{self.q_heads}] on {dev}")
         self._check(duo_pool_prefill(self.handle, layer, seqs, n, q, k, v, out, lse, self._stream(stream)),
                     "duo_pool_prefill")
         return out, lse

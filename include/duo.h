@@ -281,8 +281,11 @@ DUO_API duo_status duo_decode_attention_static_scratch(duo_cache *cache, int lay
  * attention, duo_pool_prefill, decoded with duo_pool_decode_step, branched with
  * duo_pool_fork and moved with duo_pool_copy.  Free pages are handed out lowest first.
  * Calls on one pool must be ordered on one stream; a call's launches carry the lengths and
- * pages of the moment it was made, so a captured graph repeats that call and no other.  Errors follow the cache's contract: checked
- * before any launch, lengths follow what the cache holds.
+ * pages of the moment it was made, so a captured graph repeats that call and no other
+ * (and where tokens went into a ring, a second replay starts from the ring as the first
+ * left it).
+ * Errors follow the cache's contract: checked before any launch, lengths follow what the
+ * cache holds.
  */
 typedef struct duo_pool duo_pool;
 
@@ -326,11 +329,13 @@ DUO_API duo_status duo_pool_append_kv(duo_pool *pool, int layer, int seq, const 
  *           then those of seqs[1], ... (tokens = sum of n[i]);  lse [tokens][Hq] fp32, or NULL
  * A sequence's results do not depend on the other sequences' values.  Within a sequence k
  * and v must be finite: a row that is not spoils queries that do not see it too.
- * Two launches: the attention, which reads pages, sinks, rings, k and v where they are (the
- * keys of few queries over a long history are split over CTAs, with partial rows in the
- * pool's scratch), then one that joins split rows and appends.  nseq <= 128, at most
- * 262144 tokens (else DUO_ERR_INVALID).  DUO_ERR_CAPACITY past max_len or without free
- * pages; on any error the cache is unchanged.
+ * All but lse 16-byte aligned; out and lse overlap neither the inputs nor one another nor the
+ * pool's buffer (else DUO_ERR_INVALID).  Two launches: the attention, which reads pages,
+ * sinks, rings, k and v where they are (where that shares the work out evenly, the keys of
+ * some rows are split over CTAs, with partial rows in the pool's scratch: results repeat
+ * bit for bit for the same lengths and counts), then one that joins split rows and appends.
+ * nseq <= 128, at most 262144 tokens (else DUO_ERR_INVALID).  DUO_ERR_CAPACITY past max_len
+ * or without free pages; on any error the cache is unchanged.
  */
 DUO_API duo_status duo_pool_prefill(duo_pool *pool, int layer, int nseq, const int *seqs, const int *n, const void *q,
                                     const void *k, const void *v, void *out, float *lse, void *cuda_stream);

@@ -13,7 +13,8 @@ from parity import assert_close, bits
 from test_norm_rope import freqs, reference
 from test_pool_share import _fail, _fill, _free, _listed, _pool, check_rows
 
-FAKE = 1 << 40
+FAKE, POOL = 2 << 40, 1 << 40  # tensors, and the pool's buffer (of test_pool_share)
+Q, K, V, OUT, LSE = (FAKE + (i << 36) for i in range(5))
 DEV = "cuda"
 
 
@@ -45,6 +46,24 @@ def test_ring_view_is_the_mask():
                     got = sorted(int(held[x]) for lo, hi in runs for x in range(lo, hi))
                     want = [p for p in range(S, length) if i - p < W]
                     assert got == want, (S, W, length, i, runs)
+
+
+def test_slots_are_two_runs():
+    """A row's visible slots as the kernel masks them: [0, front) and [lo, hi)."""
+    for S in (0, 1, 3, 9):
+        for W in (1, 2, 5, 8):
+            for length in range(0, 30):
+                held = oracle.ring_replay(S, W, [length])[0] if length else -np.ones(S + W, dtype=np.int64)
+                for i in range(length, length + 12):
+                    (lo1, hi1), (lo, hi) = ring_view(i, length, S, W)
+                    front = min(S, length)
+                    if lo1 == S:
+                        front = max(front, hi1)
+                    else:
+                        lo, hi = lo1, hi1
+                    got = [x for x in range(S + W) if x < front or lo <= x < hi]
+                    want = [x for x in range(S + W) if held[x] >= 0 and (held[x] < S or i - held[x] < W)]
+                    assert got == want, (S, W, length, i)
 
 
 def tiles_of(r0, rows, length, S, W):
@@ -91,9 +110,88 @@ def test_streaming_tiles_cover_what_is_visible():
         assert want <= set(tiles), (S, W, length, n, r0)
 
 
+def deal(items, sms):
+    """The host's dealing of items [(tiles, cost of one)]: (whole, ctas, shares, cuts), a share
+    (item, tile, tiles, part) per CTA, a cut (item, pieces, part0, part1)."""
+    piece, least, share_tiles = 12, 2, 2
+    cost = [t * c + piece for t, c in items]
+    n, tiles = len(items), sum(t for t, _ in items)
+    ctas = min(sms, 148, max(1, tiles // share_tiles))
+    even = -(-sum(cost) // ctas)
+    while True:
+        load, u = [0] * ctas, 0
+        while u + ctas <= n and all(load[c] + cost[u + c] <= even for c in range(ctas)):
+            for c in range(ctas):
+                load[c] += cost[u + c]
+            u += ctas
+        whole, shares, cuts, rank, t0 = u, [(0, 0, 0, 0)] * ctas, [], 0, 0
+        for c in range(ctas):
+            if u >= n:
+                break
+            room, first, tile, got = even - load[c], u, t0, 0
+            while u < n:
+                rest = items[u][0] - t0
+                can = int((room - piece) / items[u][1])  # towards zero
+                if can < min(rest, least):
+                    break
+                take = min(rest, can)
+                if rest - take < least:
+                    take = rest
+                if t0 > 0:
+                    cuts[-1][1] += 1
+                elif take < rest:
+                    cuts.append([u, 1, 2 * rank + (first != u), 2 * (rank + 1)])
+                got += take
+                room -= take * items[u][1] + piece
+                t0 += take
+                if t0 < items[u][0]:
+                    break
+                u, t0 = u + 1, 0
+            shares[c] = (first, tile, got, 2 * rank)
+            rank += got > 0
+        if u == n:
+            return whole, ctas, shares, cuts
+        even += max(1, (sum(cost[u:]) - t0 * items[u][1]) // ctas)
+
+
+def test_dealing_covers_every_tile_once():
+    """Every tile of every item goes to one CTA; the pieces of a cut item have places of their
+    own, found in order at part0, part1, part1 + 2, ...; few places, whole items in rounds."""
+    rng = np.random.default_rng(1)
+    for _ in range(400):
+        n = int(rng.choice([1, 2, 5, 40, 148, 149, 600]))
+        top = int(rng.choice([1, 2, 7, 60, 1000]))
+        items = sorted(((int(rng.integers(1, top + 1)), int(rng.choice([4, 5]))) for _ in range(n)), reverse=True)
+        sms = int(rng.choice([1, 3, 132, 148, 160]))
+        whole, ctas, shares, cuts = deal(items, sms)
+        assert 1 <= ctas <= min(sms, 148) and whole % ctas == 0 and whole <= n and len(cuts) <= ctas
+        pieces = {u: [(0, items[u][0], -1)] for u in range(whole)}
+        for first, tile, left, part in shares:  # as the kernel walks them
+            u, j = first, tile
+            while left > 0:
+                nt = min(items[u][0] - j, left)
+                pieces.setdefault(u, []).append((j, nt, -1 if nt == items[u][0] else part + (u != first)))
+                left, j, u = left - nt, 0, u + 1
+        used = [p for v in pieces.values() for _, _, p in v if p >= 0]
+        assert len(used) == len(set(used)) and all(p < 2 * 148 for p in used)
+        by_item = {c[0]: c for c in cuts}
+        for u in range(n):
+            at = 0
+            for j, nt, _ in pieces[u]:
+                assert j == at and nt >= 1
+                at += nt
+            assert at == items[u][0]
+            parts = [p for _, _, p in pieces[u]]
+            if len(parts) > 1:
+                _, count, part0, part1 = by_item[u]
+                assert parts == [part0] + [part1 + 2 * i for i in range(count - 1)]
+            else:
+                assert parts == [-1] and u not in by_item
+
+
 # ---------------------------------------------------------------- host side
 
-def _prefill(h, layer, seqs, n, q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=None):
+def _prefill(h, layer, seqs, n, q=Q, k=K, v=V, out=OUT, lse=None):
     return duo.duo_pool_prefill(h, layer, seqs, n, q, k, v, out, lse)
 
 
@@ -130,11 +228,16 @@ def test_prefill_refusals_change_nothing(dry_run):
             (I, lambda: _prefill(h, 0, [a, 3], [1, 1])), (I, lambda: _prefill(h, 0, [-1], [1])),
             (I, lambda: _prefill(h, 0, [a], [0])), (I, lambda: _prefill(h, 0, [a, b], [1, -5])),
             (I, lambda: _prefill(h, 0, [a], [300000])), (I, lambda: _prefill(h, 0, list(range(129)), [1] * 129)),
-            (I, lambda: _prefill(h, 0, [a], [1], q=None)), (I, lambda: _prefill(h, 0, [a], [1], v=FAKE + 8)),
-            (I, lambda: _prefill(h, 0, [a], [1], out=FAKE + 4)), (I, lambda: _prefill(h, 0, [a], [1], lse=FAKE + 2)),
+            (I, lambda: _prefill(h, 0, [a], [1], q=None)), (I, lambda: _prefill(h, 0, [a], [1], v=V + 8)),
+            (I, lambda: _prefill(h, 0, [a], [1], out=OUT + 4)), (I, lambda: _prefill(h, 0, [a], [1], lse=LSE + 2)),
             (I, lambda: _prefill(None, 0, [a], [1])),
-            (I, lambda: lib.duo_pool_prefill(h, 0, 1, None, one, FAKE, FAKE, FAKE, FAKE, None, None)),
-            (I, lambda: lib.duo_pool_prefill(h, 0, 1, arr, None, FAKE, FAKE, FAKE, FAKE, None, None)),
+            # results over inputs, one another or the pool
+            (I, lambda: _prefill(h, 0, [a], [1], out=Q)), (I, lambda: _prefill(h, 0, [a, b], [3, 2], out=K + 512)),
+            (I, lambda: _prefill(h, 0, [a], [1], out=V - 16)), (I, lambda: _prefill(h, 0, [a], [1], lse=OUT + 16)),
+            (I, lambda: _prefill(h, 0, [a], [1], lse=V)), (I, lambda: _prefill(h, 0, [a], [1], out=POOL + 4096)),
+            (I, lambda: _prefill(h, 0, [a], [1], q=POOL, lse=POOL + 8192)),
+            (I, lambda: lib.duo_pool_prefill(h, 0, 1, None, one, Q, K, V, OUT, None, None)),
+            (I, lambda: lib.duo_pool_prefill(h, 0, 1, arr, None, Q, K, V, OUT, None, None)),
             (C, lambda: _prefill(h, 0, [a], [601])), (C, lambda: _prefill(h, 0, [a, b], [500, 200])),
             (duo.DUO_ERR_CUDA, lambda: _fail(0, lambda: _prefill(h, 0, [a, b], [200, 300]))),
             (duo.DUO_ERR_CUDA, lambda: _fail(1, lambda: _prefill(h, 0, [a, b], [200, 300])))]:
@@ -272,6 +375,69 @@ def test_prefill_long_chunk():
     tk.prefill(0, [s, t], [4097, 1000], rows=24)
     tk.prefill(0, [t, s], [2000, 1111], rows=24)
     tk.check_cache()
+
+
+@pytest.mark.gpu
+def test_prefill_many_sequences():
+    """128 sequences in one call, most of one token; then all again."""
+    tk = Tokens(_gpu_pool(8, 2, [1, 0], 4, 60, max_seqs=128, max_len=900, num_pages=500), 7000)
+    seqs = [tk.open(x) for x in np.random.default_rng(3).integers(0, 400, 128).tolist()]
+    n = [1 + (i % 7 == 0) * i for i in range(128)]
+    tk.prefill(0, seqs, n, rows=4)
+    tk.prefill(0, seqs[::-1], n, rows=4)
+    tk.check_cache()
+
+
+@pytest.mark.gpu
+def test_prefill_many_heads():
+    """As many KV heads as a pool takes, every third one a retrieval head."""
+    tk = Tokens(_gpu_pool(128, 128, [int(h % 3 == 0) for h in range(128)], 2, 33, max_len=700, num_pages=20), 7500)
+    seqs = [tk.open(x) for x in (0, 300)]
+    tk.prefill(0, seqs, [150, 41], rows=3)
+    tk.check_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask", [[1], [0]])
+def test_prefill_largest_call(mask):
+    """The most tokens that one call takes, one query head: 1024 items, sampled rows."""
+    tk = Tokens(_gpu_pool(1, 1, mask, 16, 512, max_len=262144 + 40, num_pages=2050, max_seqs=2), 8000)
+    s = tk.open(37)
+    tk.prefill(0, [s], [262144], rows=12)
+    assert tk.pool.device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mask,replays", [([1, 0, 1, 0], 1), ([1, 1, 1, 1], 3)])
+def test_prefill_on_another_stream_and_captured(mask, replays):
+    """The call on a stream of the caller's and inside a captured graph, replayed, gives what
+    it gives eagerly: outputs and rows.  (With streaming heads a second replay would start
+    from rings in which the first has already replaced the oldest tokens; retrieval rows
+    are only written again.)"""
+    tk = Tokens(_gpu_pool(16, 4, mask, 4, 100, max_len=9000, num_pages=300), 9000)
+    s = tk.open(5000)
+    a, b, c = tk.fork(s, 3)
+    q, k, v = tk.draw(75, 16), tk.draw(75, 4), tk.draw(75, 4)
+    want = tk.pool.prefill(0, [a], [75], q, k, v)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = tk.pool.prefill(0, [b], [75], q, k, v, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    out, lse = torch.zeros_like(q), torch.zeros(75, 16, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tk.pool.prefill(0, [c], [75], q, k, v, out=out, lse=lse)
+    for _ in range(replays):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for x in (a, b, c):
+        kk, vv = tk.kv[x][0]
+        tk.kv[x][0] = (torch.cat((kk, k)), torch.cat((vv, v)))
+    tk.check_cache()
+    assert tk.pool.device_status() == 0
 
 
 @pytest.mark.gpu
