@@ -18,9 +18,9 @@
 // the same number of them (few queries over a long history are nothing but that share).
 // A cut item's CTAs leave unnormalised rows, max and sum in the scratch; the append launch
 // that follows joins them.  12 warps:
-//   warp 0      TMA: both Q tiles, then the K ring (2 stages)
+//   warp 0      TMA: the K ring (2 stages)
 //   warp 1      owns TMEM; lane 0 issues every tcgen05.mma
-//   warp 2      the V ring (2 stages); by TMA, but the last tile of a chunk row by row:
+//   warp 2      TMA: both Q tiles, the V ring (2 stages), but the last tile of a chunk row by row:
 //               rows behind it belong to the next sequence, and 0 * NaN would carry a
 //               broken neighbour's values over, so they are written as zeros
 //   warp 3      lists the CTA's pieces for the others, up to four ahead
@@ -95,12 +95,11 @@ __device__ __forceinline__ int item_of(const PoolPrefillCall &c, const PrefillLi
   w.tok0 = lists.tok0[lo];
   // heads fastest (neighbours in the grid read different heads' keys at the same places),
   // query blocks from the last -- the longest -- to the first
-  const int npos = kBM / c.G, heads = w.retr ? c.Hr : c.Hs, rem = v - first[lo];
-  const int ntq = (w.n + npos - 1) / npos, blocks = (ntq + kQT - 1) / kQT, qb = blocks - 1 - rem / heads;
-  w.idx = rem % heads;
+  const int npos = c.npos, heads = w.retr ? c.Hr : c.Hs, rem = v - first[lo], back = rem / heads;
+  w.idx = rem - back * heads;
   w.g = w.retr ? lists.retr_head[w.idx] : lists.strm_head[w.idx];
-  w.r0 = qb * kQT * npos;
-  w.nq = min(kQT, ntq - qb * kQT);
+  w.r0 = (lists.blocks[lo] - 1 - back) * kQT * npos;
+  w.nq = w.n - w.r0 > npos ? kQT : 1;
   const int k = prefill_runs(w.retr, w.len, w.n, w.r0, npos, c.S, c.W, w.runs);
   int tiles = 0;
   for (int i = 0; i < k; ++i) tiles += w.runs[i].count;
@@ -215,40 +214,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
   Piece *pieces = reinterpret_cast<Piece *>(smem + kSmMisc + 16);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const PoolLayerDesc &L = *c.layer;
-  const int npos = kBM / c.G;  // positions of a query tile
+  const int npos = c.npos;
   PrefillLists &lists = *reinterpret_cast<PrefillLists *>(smem + kSmLists);
 
-  // The prologue overlaps the end of the kernel before; what that may have written is read,
-  // and what it may read is written, behind the wait.  The lists are copied side by side:
-  // read one by one as parameters, each first touch would wait for the constant cache.
-  for (int i = tid; i < static_cast<int>(sizeof(PrefillLists) / 16); i += kThreads)
-    reinterpret_cast<uint4 *>(&lists)[i] = reinterpret_cast<const uint4 *>(&c.lists)[i];
-  if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      const bool softmax = i >= kBarPFull && i < kBarPFull + 2 * kQT, listed = i >= kBarPieceFree && i < kBarPieceFree + kPieces;
-      mbar_init(bar(i), softmax ? kBM / 32 : listed ? 3 + 4 * kQT : 1);
-    }
+  // What is done before griddepcontrol.wait overlaps the end of the kernel before: barriers,
+  // the first pieces' listing and fetching the tensor maps touch no memory of its.  The
+  // lists are copied side by side: read one by one as parameters, each first touch would
+  // wait for the constant cache.
+  static_assert(sizeof(PrefillLists) / 16 <= 2 * kThreads, "two vectors a thread");
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = tid + k * kThreads;
+    if (i < static_cast<int>(sizeof(PrefillLists) / 16))
+      reinterpret_cast<uint4 *>(&lists)[i] = reinterpret_cast<const uint4 *>(&c.lists)[i];
+  }
+  if (tid < kNumBars) {
+    const bool softmax = tid >= kBarPFull && tid < kBarPFull + 2 * kQT;
+    const bool listed = tid >= kBarPieceFree && tid < kBarPieceFree + kPieces;
+    mbar_init(bar(tid), softmax ? kBM / 32 : listed ? 3 + 4 * kQT : 1);
     fence_mbar_init();
-    *abort_flag = 0;
+    if (tid == 0) *abort_flag = 0;
   }
-  if (lane == 0 && (warp == 0 || warp == 2)) {
-    // the layer's maps live in device memory, written before this launch
-    const bool k = warp == 0;
-    for (const CUtensorMap *m : {k ? &L.tm_kr : &L.tm_vr, k ? &L.tm_ks : &L.tm_vs}) {
-      asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
-      tc::prefetch_map(m);
-    }
-    if (k) tc::prefetch_map(&c.tm_q);
-    tc::prefetch_map(k ? &c.tm_k : &c.tm_v);
-  }
-  // (tensor memory is taken behind the wait as well: a kernel before may still want some)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
-  tc::fence_before();
+  static_assert(kNumBars <= 32, "one thread a barrier");
+  if (tid >= 32 && tid < 39) tc::prefetch_map(&c.tm_q + (tid - 32));
   __syncthreads();
-  tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  uint32_t tmem = 0;
+  if (warp != 3) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 1 || warp >= kSoftWarp0) {  // (tensor memory: a kernel before may still have wanted some)
+      if (warp == 1) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+      tc::fence_before();
+      tc::named_sync(1, 32 * (1 + 4 * kQT));
+      tc::fence_after();
+      tmem = *tmem_slot;
+    }
+  }
 
   // The roles take the pieces in order: piece p is at p % kPieces while they hold it.
   auto take = [&](int p, bool &ok) -> const Piece * {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
       }
     }
   } else if (warp == 0 || warp == 2) {
-    // ================= producers: warp 0 Q and K, warp 2 V =================
+    // ================= producers: warp 0 K, warp 2 Q and V =================
     const bool is_k = warp == 0;
     const uint32_t stage0 = sbase + (is_k ? kSmK : kSmV);
     const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
@@ -316,7 +316,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
     for (int p = 0;; ++p) {
       const Piece *w = take(p, ok);
       if (!__all_sync(0xffffffffu, ok) || w->nt == 0) break;
-      const CUtensorMap *pages = is_k ? &L.tm_kr : &L.tm_vr, *slots = is_k ? &L.tm_ks : &L.tm_vs;
+      if (!is_k) {
+        if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
+          for (int q = 0; q < w->nq; ++q)
+            for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
+              tc::tma_3d(sbase + kSmQ + q * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G,
+                         w->tok0 + w->r0 + q * npos, bar(kBarQ));
+        }
+        ++queries;
+      }
+      const CUtensorMap *pages = is_k ? &c.tm_kr : &c.tm_vr, *slots = is_k ? &c.tm_ks : &c.tm_vs;
       const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
       const int *row = c.table + static_cast<int64_t>(w->slot) * c.pages_per_seq;
       Tile t = tile_at(w->runs, w->j0);
@@ -353,19 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         ++issued;
         t = next;
         page = next_page;
-        if (is_k && j == 0) {  // the queries behind the first keys: their place is free later
-          if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
-            for (int q = 0; q < w->nq; ++q)
-              for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
-                tc::tma_3d(sbase + kSmQ + q * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G,
-                           w->tok0 + w->r0 + q * npos, bar(kBarQ));
-          }
-          ++queries;
-        }
       }
       if (!ok) break;
       __syncwarp();

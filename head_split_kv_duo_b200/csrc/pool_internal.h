@@ -131,6 +131,7 @@ struct PrefillShare {
 struct alignas(16) PrefillLists {
   int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
   int tok0[kPoolMaxSeqs];        // first of the sequence's tokens in the call's tensors
+  int blocks[kPoolMaxSeqs];      // items per KV head
   int rfirst[kPoolMaxSeqs + 1], sfirst[kPoolMaxSeqs + 1];  // items before a sequence, per kind
   int unused[2];
   uint8_t retr_head[kMaxKvHeads], strm_head[kMaxKvHeads];  // KV heads of each kind
@@ -138,14 +139,14 @@ struct alignas(16) PrefillLists {
 };
 struct PoolPrefillCall {
   CUtensorMap tm_q, tm_k, tm_v;  // q [tokens][Hq][d], k and v [tokens][Hkv][d]
-  const PoolLayerDesc *layer;    // device
+  CUtensorMap tm_kr, tm_vr, tm_ks, tm_vs;  // the layer's pages, sinks and rings
   const int *table;              // device block table [max_seqs][pages_per_seq]
   int pages_per_seq;
   const char *v;
   char *out;
   float *lse, *partials;
   uint32_t *status;
-  int nseq, Hq, Hkv, G, S, W, Hr, Hs, retr_items, whole_items, ctas;
+  int nseq, Hq, Hkv, G, npos, S, W, Hr, Hs, retr_items, whole_items, ctas;  // npos: positions of a query tile
   float scale_log2;
   PrefillLists lists;
 };

@@ -318,7 +318,12 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
 
   PoolPrefillCall a{};
   PoolFinishCall f{};
-  a.layer = f.layer = P->d_layers + layer;
+  f.layer = P->d_layers + layer;
+  const PoolLayerDesc &desc = P->h_layers[layer];
+  a.tm_kr = desc.tm_kr;
+  a.tm_vr = desc.tm_vr;
+  a.tm_ks = desc.tm_ks;
+  a.tm_vs = desc.tm_vs;
   a.table = f.table = P->d_table;
   a.pages_per_seq = f.pages_per_seq = P->pages_per_seq;
   a.v = f.v = static_cast<const char *>(v);
@@ -338,7 +343,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   a.Hs = Hs;
   a.scale_log2 = P->scale * kLog2e;
   f.tokens = static_cast<int>(tokens);
-  f.npos = prefill_tile_positions(P->G);
+  a.npos = f.npos = prefill_tile_positions(P->G);
   f.npages = static_cast<int>(entries);
   int tok = 0, page = 0;
   for (int i = 0; i < nseq; ++i) {
@@ -374,8 +379,9 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     a.lists.len[i] = f.len[s];
     a.lists.n[i] = f.n[s];
     a.lists.tok0[i] = f.tok0[s];
+    a.lists.blocks[i] = prefill_blocks(n[s], P->G);
   }
-  const HeadMap &hm = P->h_layers[layer].hm;
+  const HeadMap &hm = desc.hm;
   std::copy(hm.retr_head, hm.retr_head + Hr, a.lists.retr_head);
   std::copy(hm.strm_head, hm.strm_head + Hs, a.lists.strm_head);
   a.retr_items = a.lists.rfirst[nseq];

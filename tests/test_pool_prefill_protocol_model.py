@@ -51,6 +51,10 @@ def cta(sim, pieces, q_waits=True, ring_waits=True, pv_before_next_s=True):
             nt, _ = take(p)
             if nt == 0:
                 return
+            if not is_k:
+                if p > 0 and q_waits:
+                    yield wait("QEmpty", p - 1)
+                sim.spawn(load("q", ("Q", p), "Q"), f"tmaQ{p}")
             for j in range(nt):
                 s = issued % KST
                 if issued >= KST:
@@ -58,10 +62,6 @@ def cta(sim, pieces, q_waits=True, ring_waits=True, pv_before_next_s=True):
                 take(p)
                 sim.spawn(load(f"{name}{s}", (name, p, j), f"{full}{s}"), f"tma{name}{p}.{j}")
                 issued += 1
-                if is_k and j == 0:
-                    if p > 0 and q_waits:
-                        yield wait("QEmpty", p - 1)
-                    sim.spawn(load("q", ("Q", p), "Q"), f"tmaQ{p}")
                 yield None
             sim.arrive(f"Free{p % RING}")
             p += 1
