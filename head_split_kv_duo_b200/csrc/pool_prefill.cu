@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_c
 // gets more than its even share of the cost, so that neighbours read the same keys at about
 // the same time; then the rest, cut where a CTA's share is full.  Costs are in quarters of a
 // retrieval head's key tile (2650 cycles): a streaming head's tile, masked for the most part,
-// is five, and a piece twelve more than its tiles (queries, the first product, masks at
+// is five, and a piece sixteen more than its tiles (queries, the first product, masks at
 // its ends, the rows' way out).
 // Pieces of fewer than two tiles are avoided, and a short call runs on as many CTAs as have
 // two tiles each.
@@ -223,7 +223,7 @@ struct Deal {
   };
   std::vector<Cut> cuts;
 };
-constexpr int kTileCost = 4, kStreamingTileCost = 5, kPieceCost = 12;
+constexpr int kTileCost = 4, kStreamingTileCost = 5, kPieceCost = 16;
 void deal_items(const std::vector<Item> &items, int sms, Deal *d) {
   constexpr int kLeast = 2, kShareTiles = 2;
   const int n = static_cast<int>(items.size());

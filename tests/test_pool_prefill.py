@@ -113,7 +113,7 @@ def test_streaming_tiles_cover_what_is_visible():
 def deal(items, sms):
     """The host's dealing of items [(tiles, cost of one)]: (whole, ctas, shares, cuts), a share
     (item, tile, tiles, part) per CTA, a cut (item, pieces, part0, part1)."""
-    piece, least, share_tiles = 12, 2, 2
+    piece, least, share_tiles = 16, 2, 2
     cost = [t * c + piece for t, c in items]
     n, tiles = len(items), sum(t for t, _ in items)
     ctas = min(sms, 148, max(1, tiles // share_tiles))
