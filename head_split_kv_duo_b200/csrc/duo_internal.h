@@ -261,28 +261,4 @@ cudaError_t launch_pool_chunk_append(const PoolChunkAppend &c, int Hr, int Hs, c
 // decode tiling shared by host (split sizing) and device
 int decode_tokens_per_stage(duo_dtype dt, int D, bool int4);
 
-// A byte range of a call's tensors, for its overlap check.
-struct Span {
-  uintptr_t lo, hi;
-  bool meets(const Span &o) const { return lo < o.hi && o.lo < hi; }
-};
-
-// A launch whose start may overlap the end of the kernel before it in the stream: the
-// kernel executes griddepcontrol.wait before it reads or writes global memory.
-template <class Param>
-cudaError_t launch_overlapped(void (*kernel)(Param), int64_t blocks, int threads, int smem, cudaStream_t st,
-                              const Param &param) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, param);
-}
-
 }  // namespace duo

@@ -32,6 +32,7 @@
 #include <cmath>
 #include <new>
 
+#include "call_common.h"
 #include "device_common.cuh"
 #include "nvtx_range.h"
 

@@ -64,6 +64,17 @@ constexpr int kBarQ = 0, kBarQEmpty = 1, kBarKFull = 2, kBarKEmpty = kBarKFull +
               kBarDrain = kBarPieceFree + kPieces, kNumBars = kBarDrain + 1;
 static_assert(kNumBars * 8 <= 256 && kSmemAlloc <= 227 * 1024, "shared memory");
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // A piece of a CTA's work: key tiles [j0, j0 + nt) of an item.
 struct Piece {
   int g, idx, retr;     // KV head, its index among heads of its kind
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
       ok = wait(kBarQ, p) && wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
       if (!ok) break;
       tc::fence_after();
-      if (tc::elect()) {
+      if (elect()) {
         issue_s(0, k_tile % kKStages);
         if (nq > 1) issue_s(1, k_tile % kKStages);
         tc::commit(bar(kBarKEmpty + k_tile % kKStages));
@@ -437,13 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
           if (ok) ok = wait(kBarPFull + t, p_tile[t]);
           if (!ok) break;
           tc::fence_after();
-          if (tc::elect()) issue_pv(t, v_tile % kVStages, j == 0, 0, kPFirst / 16);
+          if (elect()) issue_pv(t, v_tile % kVStages, j == 0, 0, kPFirst / 16);
           __syncwarp();
           ok = wait(kBarPRest + t, p_tile[t]);
           ++p_tile[t];
           if (!ok) break;
           tc::fence_after();
-          if (tc::elect()) {
+          if (elect()) {
             issue_pv(t, v_tile % kVStages, false, kPFirst / 16, 8);
             if (t == nq - 1) tc::commit(bar(kBarVEmpty + v_tile % kVStages));
             if (j + 1 == nt) {
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
       }
     }
     // every MMA issued has completed before TMEM is freed
-    if (tc::elect()) {
+    if (elect()) {
       tc::commit(bar(kBarDrain));
       mbar_wait(bar(kBarDrain), 0, c.status);
     }

@@ -6,7 +6,7 @@
 #include <functional>
 #include <vector>
 
-#include "duo_internal.h"
+#include "call_common.h"
 
 struct duo_pool {
   int layers = 0, Hkv = 0, Hq = 0, G = 0, D = 0, S = 0, W = 0, max_seqs = 0, pages_per_seq = 0;
