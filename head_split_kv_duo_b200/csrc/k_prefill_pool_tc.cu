@@ -19,7 +19,7 @@
 // A cut item's CTAs leave unnormalised rows, max and sum in the scratch; the append launch
 // that follows joins them.  12 warps:
 //   warp 0      TMA: the K ring (2 stages)
-//   warp 1      owns TMEM; lane 0 issues every tcgen05.mma
+//   warp 1      owns TMEM; one elected lane issues every tcgen05.mma
 //   warp 2      TMA: both Q tiles, the V ring (2 stages), but the last tile of a chunk row by row:
 //               rows behind it belong to the next sequence, and 0 * NaN would carry a
 //               broken neighbour's values over, so they are written as zeros
@@ -35,6 +35,25 @@
 //
 // Every mbarrier wait is bounded; one that runs out latches kDevTimeout, and every role
 // drains and exits.
+//
+// Bound: a pair of tiles (256 rows x 128 keys) costs 2048 cycles of the tensor core and as
+// many of MUFU (exponentials of two warps per scheduler); it takes about 2650, and long
+// calls run at the power limit (1.66 GHz).  8 KV heads (4 of them retrieval heads) of 4
+// query heads, alone on the GPU with the append:
+//   8192 tokens on 24576: 1.51 ms, 1.30 PFLOP/s (back to back, at 1.45 GHz, 1.75 ms)
+//   64 tokens on 131000: 73 us (0.27 GB and 69 GFLOP: 41 us at either rate)
+// Steps from a first version of 1.89 ms and 84 us (one CTA per item, the maximum before the
+// exponentials, P handed over whole, lane 0 alone issuing), in that order:
+//   products of a tile's first 96 keys start before the other 32 are done, the maximum is
+//   checked beside the exponentials, K and V are waited for before P, the issuing warp runs
+//   on uniform values (issue 3700 -> 2000 cycles a pair of tiles): 1.61 ms
+//   rows out through shared memory, partial rows transposed, masks as two runs: 1.55 ms
+//   one site each for listing and storing (84 -> 75 KB of code: the loops then stay in the
+//   instruction cache): 1.51 ms
+//   even shares by cost: 630 -> 340 us for eight sequences of very different lengths
+// Without gain: part of the exponentials as polynomials on the FMA pipe (1.55 to 1.76 ms for
+// an eighth to a third of them), P in halves (1.65) or whole (1.54), tiles fetched into L2
+// ahead of their loads (73 -> 85 us), listing pieces with a function call.
 #include "pool_internal.h"
 #include "tcgen05.cuh"
 
@@ -54,14 +73,14 @@ constexpr int kSmMisc = kSmBar + 256;
 constexpr int kPieces = 4;  // pieces listed ahead
 constexpr int kSmOut = kSmMisc + 768;  // per softmax warp: 32 rows' 32 dims on their way out
 constexpr int kSmLists = kSmOut + 4 * kQT * 2048;
-constexpr int kSmemAlloc = kSmLists + static_cast<int>(sizeof(PrefillLists)) + 1024;  // slack for aligning the base to 1 KiB
+constexpr int kSmemAlloc = kSmLists + static_cast<int>(sizeof(PrefillLists)) + 1024;  // slack: the base at 1 KiB
 constexpr int kTmS = 0, kTmO = 256;
 constexpr int kPFirst = 96;  // keys of a tile whose P is handed over first
 
-constexpr int kBarQ = 0, kBarQEmpty = 1, kBarKFull = 2, kBarKEmpty = kBarKFull + kKStages, kBarVFull = kBarKEmpty + kKStages,
-              kBarVEmpty = kBarVFull + kVStages, kBarSFull = kBarVEmpty + kVStages, kBarPFull = kBarSFull + kQT,
-              kBarPRest = kBarPFull + kQT, kBarOFull = kBarPRest + kQT, kBarPiece = kBarOFull + kQT, kBarPieceFree = kBarPiece + kPieces,
-              kBarDrain = kBarPieceFree + kPieces, kNumBars = kBarDrain + 1;
+constexpr int kBarQ = 0, kBarQEmpty = 1, kBarKFull = 2, kBarKEmpty = kBarKFull + kKStages,
+              kBarVFull = kBarKEmpty + kKStages, kBarVEmpty = kBarVFull + kVStages, kBarSFull = kBarVEmpty + kVStages,
+              kBarPFull = kBarSFull + kQT, kBarPRest = kBarPFull + kQT, kBarOFull = kBarPRest + kQT,
+              kBarPiece = kBarOFull + kQT, kBarPieceFree = kBarPiece + kPieces, kBarDrain = kBarPieceFree + kPieces, kNumBars = kBarDrain + 1;
 static_assert(kNumBars * 8 <= 256 && kSmemAlloc <= 227 * 1024, "shared memory");
 
 // True in one lane of a converged warp, the same one every time.
@@ -203,7 +222,8 @@ __device__ __forceinline__ float probabilities(const float (&v)[128], float c, f
 
 // A V tile whose rows from `valid` on are not the sequence's: a warp copies its rows and
 // writes zeros behind them, in the layout a swizzled TMA load leaves.
-__device__ __forceinline__ void copy_ragged_tile(const char *src, int64_t row_bytes, int valid, uint32_t dst, int lane) {
+__device__ __forceinline__ void copy_ragged_tile(const char *src, int64_t row_bytes, int valid, uint32_t dst,
+                                                 int lane) {
   for (int i = lane; i < kBN * 16; i += 32) {
     const int row = i >> 4, chunk = i & 15;
     const uint32_t to = dst + (chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
@@ -270,218 +290,217 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
 
   // Shares of the launch's 384 * 168 registers: the softmax warps hold a row of logits.
   if (warp < kSoftWarp0) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == 3) {
-    // ================= lists the pieces =================
-    if (lane == 0) {
-      int p = 0;
-      bool ok = true;
-      auto slot = [&]() -> Piece * {
-        if (p >= kPieces)
-          ok = tc::wait_bar(bar(kBarPieceFree + p % kPieces), (p / kPieces - 1) & 1, c.status, abort_flag);
-        return ok ? pieces + p % kPieces : nullptr;
-      };
-      auto publish = [&] {
-        mbar_arrive(bar(kBarPiece + p % kPieces));
-        ++p;
-      };
-      const PrefillShare sh = lists.share[blockIdx.x];
-      int u = blockIdx.x, j0 = 0, left = sh.tiles;
-      while (ok) {
-        const bool whole = u < c.whole_items;
-        if (!whole && left == sh.tiles) {  // on to the share
-          u = sh.item;
-          j0 = sh.tile;
-        }
-        if (!whole && left == 0) break;
-        Piece *w = slot();
-        if (!ok) break;
-        const int tiles = item_of(c, lists, u, *w), nt = whole ? tiles : min(tiles - j0, left);
-        w->j0 = j0;
-        w->nt = nt;
-        w->part = nt == tiles ? -1 : (u == sh.item ? sh.part : sh.part + 1);
-        publish();
-        u += whole ? gridDim.x : 1;
-        if (!whole) {
-          left -= nt;
-          j0 = 0;
-        }
-      }
-      if (ok) {
-        Piece *w = slot();
-        if (ok) {
-          w->nt = 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 3) {
+      // ================= lists the pieces =================
+      if (lane == 0) {
+        int p = 0;
+        bool ok = true;
+        auto slot = [&]() -> Piece * {
+          if (p >= kPieces)
+            ok = tc::wait_bar(bar(kBarPieceFree + p % kPieces), (p / kPieces - 1) & 1, c.status, abort_flag);
+          return ok ? pieces + p % kPieces : nullptr;
+        };
+        auto publish = [&] {
+          mbar_arrive(bar(kBarPiece + p % kPieces));
+          ++p;
+        };
+        const PrefillShare sh = lists.share[blockIdx.x];
+        int u = blockIdx.x, j0 = 0, left = sh.tiles;
+        while (ok) {
+          const bool whole = u < c.whole_items;
+          if (!whole && left == sh.tiles) {  // on to the share
+            u = sh.item;
+            j0 = sh.tile;
+          }
+          if (!whole && left == 0) break;
+          Piece *w = slot();
+          if (!ok) break;
+          const int tiles = item_of(c, lists, u, *w), nt = whole ? tiles : min(tiles - j0, left);
+          w->j0 = j0;
+          w->nt = nt;
+          w->part = nt == tiles ? -1 : (u == sh.item ? sh.part : sh.part + 1);
           publish();
-        }
-      }
-    }
-  } else if (warp == 0 || warp == 2) {
-    // ================= producers: warp 0 K, warp 2 Q and V =================
-    const bool is_k = warp == 0;
-    const uint32_t stage0 = sbase + (is_k ? kSmK : kSmV);
-    const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
-    constexpr int kStages = kKStages;
-    static_assert(kKStages == kVStages, "one producer loop for both rings");
-    int issued = 0, queries = 0;
-    bool ok = true;
-    for (int p = 0;; ++p) {
-      const Piece *w = take(p, ok);
-      if (!__all_sync(0xffffffffu, ok) || w->nt == 0) break;
-      if (!is_k) {
-        if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
-          for (int q = 0; q < w->nq; ++q)
-            for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
-              tc::tma_3d(sbase + kSmQ + q * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G,
-                         w->tok0 + w->r0 + q * npos, bar(kBarQ));
-        }
-        ++queries;
-      }
-      const CUtensorMap *pages = is_k ? &c.tm_kr : &c.tm_vr, *slots = is_k ? &c.tm_ks : &c.tm_vs;
-      const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
-      const int *row = c.table + static_cast<int64_t>(w->slot) * c.pages_per_seq;
-      Tile t = tile_at(w->runs, w->j0);
-      int page = t.src == kPages ? row[t.y / kBN] : 0;
-      for (int j = 0; j < w->nt; ++j) {
-        const int s = issued % kStages;
-        // the next tile's page number is on its way while this one waits for its stage
-        Tile next = t;
-        int next_page = 0;
-        if (j + 1 < w->nt) {
-          next = tile_at(w->runs, w->j0 + j + 1);
-          if (next.src == kPages) next_page = row[next.y / kBN];
-        }
-        if (lane == 0 && issued >= kStages)
-          ok = tc::wait_bar(bar(empty0 + s), ((issued / kStages) - 1) & 1, c.status, abort_flag);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
-        if (!ok) break;
-        const uint32_t dst = stage0 + s * kTile, fb = bar(full0 + s);
-        const int valid = t.src == kChunk ? w->n - t.y : kBN;
-        if (!is_k && valid < kBN) {
-          copy_ragged_tile(c.v + (static_cast<int64_t>(w->tok0 + t.y) * c.Hkv + w->g) * 256,
-                           static_cast<int64_t>(c.Hkv) * 256, valid, dst, lane);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(fb);
-        } else if (lane == 0) {
-          mbar_expect_tx(fb, kTile);
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t to = dst + h * kHalf;
-            if (t.src == kPages) tc::tma_3d(to, pages, 64 * h, 0, page * c.Hr + w->idx, fb);
-            else if (t.src == kSlots) tc::tma_3d(to, slots, 64 * h, t.y, w->slot * c.Hs + w->idx, fb);
-            else tc::tma_3d(to, chunk, 64 * h, w->g, w->tok0 + t.y, fb);
+          u += whole ? gridDim.x : 1;
+          if (!whole) {
+            left -= nt;
+            j0 = 0;
           }
         }
-        ++issued;
-        t = next;
-        page = next_page;
+        if (ok) {
+          Piece *w = slot();
+          if (ok) {
+            w->nt = 0;
+            publish();
+          }
+        }
       }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) leave(p);
-    }
-    if (lane == 0) {  // nothing may still be landing in shared memory when the CTA ends
-      if (queries > 0) mbar_wait(bar(kBarQ), (queries - 1) & 1, c.status);
-      tc::drain_loads(bar(full0), kStages, issued, c.status);
-    }
-  } else {
-    // ================= MMA issuer =================
-    // The warp runs the loop as one, on values that are the same in all its lanes, and one
-    // elected lane issues: descriptors then stay in uniform registers.  (With lane 0 alone
-    // in the loop the tensor pipe waited for its issue: see the times above.)
-    constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, false, false);
-    constexpr uint32_t kIdPV = tc::idesc_bf16(kBM, kD, false, true);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    // operands lie below 256 KiB, so one at byte offset o is the base's descriptor + (o >> 4)
-    const uint64_t qd0 = tc::sdesc(sbase + kSmQ, 16, 1024), kd0 = tc::sdesc(sbase + kSmK, 16, 1024);
-    const uint64_t vd0 = tc::sdesc(sbase + kSmV, kHalf, 1024);
-    auto wait = [&](int b, int phase) {
-      return __all_sync(0xffffffffu, tc::wait_bar(bar(b), phase & 1, c.status, abort_flag)) != 0;
-    };
-    // S_t = Q_t K^T with the K tile of stage s, d 128 in 8 steps of 16
-    auto issue_s = [&](int t, int s) {
-      const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + s * (kTile >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-        tc::mma_ss(tm + kTmS + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
-      }
-      tc::commit(bar(kBarSFull + t));
-    };
-    // O_t (+)= P_t V with the V tile of stage s, 128 keys in 8 steps of 16
-    auto issue_pv = [&](int t, int s, bool first, int from, int to) {
-      const uint64_t vd = vd0 + s * (kTile >> 4);
-#pragma unroll
-      for (int kk = from; kk < to; ++kk)
-        tc::mma_ts(tm + kTmO + t * 128, tm + kTmS + t * 128 + kk * 8, vd + kk * (2048 >> 4), kIdPV,
-                   kk > 0 || !first ? 1u : 0u);
-    };
-    bool ok = true;
-    int k_tile = 0, v_tile = 0, p_tile[kQT] = {0, 0};
-    for (int p = 0;; ++p) {
-      const Piece *w = take(p, ok);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const int nt = __shfl_sync(0xffffffffu, w->nt, 0), nq = __shfl_sync(0xffffffffu, w->nq, 0);
-      if (lane == 0) leave(p);
-      if (nt == 0) break;
-      ok = wait(kBarQ, p) && wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
-      if (!ok) break;
-      tc::fence_after();
-      if (elect()) {
-        issue_s(0, k_tile % kKStages);
-        if (nq > 1) issue_s(1, k_tile % kKStages);
-        tc::commit(bar(kBarKEmpty + k_tile % kKStages));
-        if (nt == 1) tc::commit(bar(kBarQEmpty));
-      }
-      __syncwarp();
-      ++k_tile;
-      for (int j = 0; j < nt && ok; ++j) {
-#pragma unroll
-        for (int t = 0; t < kQT; ++t) {
-          if (t >= nq || !ok) break;
-          // K and V first: they are there long before P, and only P should be waited for
-          if (t == 0) ok = wait(kBarVFull + v_tile % kVStages, v_tile / kVStages);
-          if (ok && t == 0 && j + 1 < nt) ok = wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
-          if (ok) ok = wait(kBarPFull + t, p_tile[t]);
+    } else if (warp == 0 || warp == 2) {
+      // ================= producers: warp 0 K, warp 2 Q and V =================
+      const bool is_k = warp == 0;
+      const uint32_t stage0 = sbase + (is_k ? kSmK : kSmV);
+      const int full0 = is_k ? kBarKFull : kBarVFull, empty0 = is_k ? kBarKEmpty : kBarVEmpty;
+      constexpr int kStages = kKStages;
+      static_assert(kKStages == kVStages, "one producer loop for both rings");
+      int issued = 0, queries = 0;
+      bool ok = true;
+      for (int p = 0;; ++p) {
+        const Piece *w = take(p, ok);
+        if (!__all_sync(0xffffffffu, ok) || w->nt == 0) break;
+        if (!is_k) {
+          if (lane == 0 && p > 0) ok = tc::wait_bar(bar(kBarQEmpty), (p - 1) & 1, c.status, abort_flag);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
           if (!ok) break;
-          tc::fence_after();
-          if (elect()) issue_pv(t, v_tile % kVStages, j == 0, 0, kPFirst / 16);
-          __syncwarp();
-          ok = wait(kBarPRest + t, p_tile[t]);
-          ++p_tile[t];
+          if (lane == 0) {
+            mbar_expect_tx(bar(kBarQ), 256 * c.G * npos * w->nq);
+            for (int q = 0; q < w->nq; ++q)
+              for (int h = 0; h < 2; ++h)  // box: 64 dims x G heads x npos positions
+                tc::tma_3d(sbase + kSmQ + q * kTile + h * kHalf, &c.tm_q, 64 * h, w->g * c.G,
+                           w->tok0 + w->r0 + q * npos, bar(kBarQ));
+          }
+          ++queries;
+        }
+        const CUtensorMap *pages = is_k ? &c.tm_kr : &c.tm_vr, *slots = is_k ? &c.tm_ks : &c.tm_vs;
+        const CUtensorMap *chunk = is_k ? &c.tm_k : &c.tm_v;
+        const int *row = c.table + static_cast<int64_t>(w->slot) * c.pages_per_seq;
+        Tile t = tile_at(w->runs, w->j0);
+        int page = t.src == kPages ? row[t.y / kBN] : 0;
+        for (int j = 0; j < w->nt; ++j) {
+          const int s = issued % kStages;
+          // the next tile's page number is on its way while this one waits for its stage
+          Tile next = t;
+          int next_page = 0;
+          if (j + 1 < w->nt) {
+            next = tile_at(w->runs, w->j0 + j + 1);
+            if (next.src == kPages) next_page = row[next.y / kBN];
+          }
+          if (lane == 0 && issued >= kStages)
+            ok = tc::wait_bar(bar(empty0 + s), ((issued / kStages) - 1) & 1, c.status, abort_flag);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
           if (!ok) break;
-          tc::fence_after();
-          if (elect()) {
-            issue_pv(t, v_tile % kVStages, false, kPFirst / 16, 8);
-            if (t == nq - 1) tc::commit(bar(kBarVEmpty + v_tile % kVStages));
-            if (j + 1 == nt) {
-              tc::commit(bar(kBarOFull + t));
-            } else {
-              issue_s(t, k_tile % kKStages);
-              if (t == nq - 1) {
-                tc::commit(bar(kBarKEmpty + k_tile % kKStages));
-                if (j + 2 == nt) tc::commit(bar(kBarQEmpty));
-              }
+          const uint32_t dst = stage0 + s * kTile, fb = bar(full0 + s);
+          const int valid = t.src == kChunk ? w->n - t.y : kBN;
+          if (!is_k && valid < kBN) {
+            copy_ragged_tile(c.v + (static_cast<int64_t>(w->tok0 + t.y) * c.Hkv + w->g) * 256,
+                             static_cast<int64_t>(c.Hkv) * 256, valid, dst, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fb);
+          } else if (lane == 0) {
+            mbar_expect_tx(fb, kTile);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t to = dst + h * kHalf;
+              if (t.src == kPages) tc::tma_3d(to, pages, 64 * h, 0, page * c.Hr + w->idx, fb);
+              else if (t.src == kSlots) tc::tma_3d(to, slots, 64 * h, t.y, w->slot * c.Hs + w->idx, fb);
+              else tc::tma_3d(to, chunk, 64 * h, w->g, w->tok0 + t.y, fb);
             }
           }
-          __syncwarp();
-          if (t == nq - 1) {
-            ++v_tile;
-            if (j + 1 < nt) ++k_tile;
+          ++issued;
+          t = next;
+          page = next_page;
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) leave(p);
+      }
+      if (lane == 0) {  // nothing may still be landing in shared memory when the CTA ends
+        if (queries > 0) mbar_wait(bar(kBarQ), (queries - 1) & 1, c.status);
+        tc::drain_loads(bar(full0), kStages, issued, c.status);
+      }
+    } else {
+      // ================= MMA issuer =================
+      // The warp runs the loop as one, on values that are the same in all its lanes, and one
+      // elected lane issues: descriptors then stay in uniform registers.
+      constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, false, false);
+      constexpr uint32_t kIdPV = tc::idesc_bf16(kBM, kD, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // operands lie below 256 KiB, so one at byte offset o is the base's descriptor + (o >> 4)
+      const uint64_t qd0 = tc::sdesc(sbase + kSmQ, 16, 1024), kd0 = tc::sdesc(sbase + kSmK, 16, 1024);
+      const uint64_t vd0 = tc::sdesc(sbase + kSmV, kHalf, 1024);
+      auto wait = [&](int b, int phase) {
+        return __all_sync(0xffffffffu, tc::wait_bar(bar(b), phase & 1, c.status, abort_flag)) != 0;
+      };
+      // S_t = Q_t K^T with the K tile of stage s, d 128 in 8 steps of 16
+      auto issue_s = [&](int t, int s) {
+        const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + s * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          tc::mma_ss(tm + kTmS + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
+        }
+        tc::commit(bar(kBarSFull + t));
+      };
+      // O_t (+)= P_t V with the V tile of stage s, 128 keys in 8 steps of 16
+      auto issue_pv = [&](int t, int s, bool first, int from, int to) {
+        const uint64_t vd = vd0 + s * (kTile >> 4);
+#pragma unroll
+        for (int kk = from; kk < to; ++kk)
+          tc::mma_ts(tm + kTmO + t * 128, tm + kTmS + t * 128 + kk * 8, vd + kk * (2048 >> 4), kIdPV,
+                     kk > 0 || !first ? 1u : 0u);
+      };
+      bool ok = true;
+      int k_tile = 0, v_tile = 0, p_tile[kQT] = {0, 0};
+      for (int p = 0;; ++p) {
+        const Piece *w = take(p, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int nt = __shfl_sync(0xffffffffu, w->nt, 0), nq = __shfl_sync(0xffffffffu, w->nq, 0);
+        if (lane == 0) leave(p);
+        if (nt == 0) break;
+        ok = wait(kBarQ, p) && wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
+        if (!ok) break;
+        tc::fence_after();
+        if (elect()) {
+          issue_s(0, k_tile % kKStages);
+          if (nq > 1) issue_s(1, k_tile % kKStages);
+          tc::commit(bar(kBarKEmpty + k_tile % kKStages));
+          if (nt == 1) tc::commit(bar(kBarQEmpty));
+        }
+        __syncwarp();
+        ++k_tile;
+        for (int j = 0; j < nt && ok; ++j) {
+#pragma unroll
+          for (int t = 0; t < kQT; ++t) {
+            if (t >= nq || !ok) break;
+            // K and V first: they are there long before P, and only P should be waited for
+            if (t == 0) ok = wait(kBarVFull + v_tile % kVStages, v_tile / kVStages);
+            if (ok && t == 0 && j + 1 < nt) ok = wait(kBarKFull + k_tile % kKStages, k_tile / kKStages);
+            if (ok) ok = wait(kBarPFull + t, p_tile[t]);
+            if (!ok) break;
+            tc::fence_after();
+            if (elect()) issue_pv(t, v_tile % kVStages, j == 0, 0, kPFirst / 16);
+            __syncwarp();
+            ok = wait(kBarPRest + t, p_tile[t]);
+            ++p_tile[t];
+            if (!ok) break;
+            tc::fence_after();
+            if (elect()) {
+              issue_pv(t, v_tile % kVStages, false, kPFirst / 16, 8);
+              if (t == nq - 1) tc::commit(bar(kBarVEmpty + v_tile % kVStages));
+              if (j + 1 == nt) {
+                tc::commit(bar(kBarOFull + t));
+              } else {
+                issue_s(t, k_tile % kKStages);
+                if (t == nq - 1) {
+                  tc::commit(bar(kBarKEmpty + k_tile % kKStages));
+                  if (j + 2 == nt) tc::commit(bar(kBarQEmpty));
+                }
+              }
+            }
+            __syncwarp();
+            if (t == nq - 1) {
+              ++v_tile;
+              if (j + 1 < nt) ++k_tile;
+            }
           }
         }
       }
+      // every MMA issued has completed before TMEM is freed
+      if (elect()) {
+        tc::commit(bar(kBarDrain));
+        mbar_wait(bar(kBarDrain), 0, c.status);
+      }
+      __syncwarp();
     }
-    // every MMA issued has completed before TMEM is freed
-    if (elect()) {
-      tc::commit(bar(kBarDrain));
-      mbar_wait(bar(kBarDrain), 0, c.status);
-    }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ================= softmax of query tile qt: one thread per query row =================

@@ -290,8 +290,10 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   }
   if (tokens > kPrefillMaxTokens) return DUO_ERR_INVALID;
   {  // the results overlap neither the inputs, nor one another, nor the pool
-    auto span = [&](const void *p, int64_t bytes) { return Span{reinterpret_cast<uintptr_t>(p),
-                                                                reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(p ? bytes : 0)}; };
+    auto span = [](const void *p, int64_t bytes) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      return Span{at, at + static_cast<uintptr_t>(p ? bytes : 0)};
+    };
     const int64_t qb = tokens * P->Hq * 256, kb = tokens * P->Hkv * 256;
     const Span o = span(out, qb), l = span(lse, tokens * P->Hq * 4);
     if (o.meets(l)) return DUO_ERR_INVALID;
@@ -399,7 +401,8 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     const int at = static_cast<int>(std::upper_bound(first, first + nseq, u) - first) - 1;
     const int rem = u - first[at];
     f.cuts[i] = {order[at], prefill_blocks(n[order[at]], P->G) - 1 - rem / heads,
-                 retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1, f.join_blocks};
+                 retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1,
+                 f.join_blocks};
     f.join_blocks += kJoinGroups * join_threads(cut.pieces);
   }
   if (!dry_run() && prepare_prefill_pool_tc(&a, q, k, v, f.tokens) != cudaSuccess) return DUO_ERR_CUDA;

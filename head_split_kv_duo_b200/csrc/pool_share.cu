@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(256) pool_share_kernel(const __grid_constant__
     if (page < c.npages) {
       const int64_t left = c.len - static_cast<int64_t>(c.page0 + page) * kPoolTile - row0;
       const int valid = static_cast<int>(left < 0 ? 0 : left < kShareRows ? left : kShareRows);
-      const char *src = (kv ? A.rv : A.rk) + ((static_cast<int64_t>(c.list[page]) * A.Hr + idx) * kPoolTile + row0) * 256;
+      const char *src =
+          (kv ? A.rv : A.rk) + ((static_cast<int64_t>(c.list[page]) * A.Hr + idx) * kPoolTile + row0) * 256;
       char *base = kv ? B.rv : B.rk;
       const int *to = c.list + c.npages + page * c.ndst;
       copy_piece<kShareRows>(src, kShareRows, valid, c.ndst, [&](int d) {
@@ -155,7 +156,8 @@ duo_status share_sequence(const duo_pool *P, int seq, duo_pool *Q, int shared, i
       for (int d = 0; d < n; ++d) c.list[c.npages + i * n + d] = lists[d][c.page0 + i];
     }
     auto blocks = [&](int rows) {
-      c.pieces = std::max(std::max(c.npages * (kPoolTile / rows), c.ring_rows >= 0 ? (P->S + P->W + rows - 1) / rows : 1), 1);
+      const int ring = c.ring_rows >= 0 ? (P->S + P->W + rows - 1) / rows : 1;
+      c.pieces = std::max({c.npages * (kPoolTile / rows), ring, 1});
       return static_cast<int64_t>(P->layers) * c.heads2 * c.pieces;
     };
     // 64 rows a piece stream best (32900 tokens of 8 layers 170 us, 197 with 32); where that
