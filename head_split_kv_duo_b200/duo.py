@@ -644,18 +644,18 @@ class DuoRope:
             pass
 
     def _side(self, x, out, name, n, dtype, device):
-        """(stride, out) of one of q, k, v [n][heads][head_dim], its tokens any stride apart."""
+        """(heads, stride, out) of one of q, k, v [n][heads][head_dim], its tokens any stride apart."""
         shape, strides, d = x.shape, x.stride(), self.head_dim
         h = shape[1] if len(shape) == 3 else 0
         if h < 1 or shape[0] != n or shape[2] != d or strides[2] != 1 or (h > 1 and strides[1] != d) or \
-                x.dtype != dtype or x.device != device:
-            raise ValueError(f"{name}: expected {dtype} [{n}][heads][{d}] on {device}, each token's rows "
+                x.dtype != dtype or x.get_device() != device:
+            raise ValueError(f"{name}: expected {dtype} [{n}][heads][{d}] on cuda:{device}, each token's rows "
                              f"dense, got {x.dtype} {tuple(shape)} with strides {strides} on {x.device}")
         if out is None:
             out = x.new_empty((n, h, d))
-        elif out.dtype != dtype or out.device != device or out.shape != shape or not out.is_contiguous():
-            raise ValueError(f"{name}_out: expected contiguous {dtype} {tuple(shape)} on {device}")
-        return (strides[0] if n > 1 else h * d), out
+        elif out.dtype != dtype or out.get_device() != device or out.shape != shape or not out.is_contiguous():
+            raise ValueError(f"{name}_out: expected contiguous {dtype} {tuple(shape)} on cuda:{device}")
+        return h, (strides[0] if n > 1 else h * d), out
 
     def norm_rope(self, q, k, positions, v=None, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None,
                   v_out=None, stream=None):
@@ -664,30 +664,31 @@ class DuoRope:
         x = q if q is not None else k
         if x is None:
             raise ValueError("q or k is needed")
-        n, dtype, device = x.shape[0], x.dtype, x.device
-        if dtype not in _DTYPES or device.type != "cuda" or device.index != torch.cuda.current_device():
-            raise ValueError(f"expected bf16 or fp32 tensors on the current CUDA device, got {dtype} on {device}")
-        if positions.dtype != torch.int32 or positions.device != device or not positions.is_contiguous() or \
-                tuple(positions.shape) not in (((self.axes, n),) if self.axes > 1 else ((1, n), (n,))):
-            raise ValueError(f"positions: expected contiguous int32 [{self.axes}][{n}] on {device}, got "
-                             f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
+        n, dtype, device = x.shape[0], x.dtype, x.get_device()
+        code = _DTYPES.get(dtype)
+        if code is None or device < 0 or device != torch.cuda.current_device():
+            raise ValueError(f"expected bf16 or fp32 tensors on the current CUDA device, got {dtype} on {x.device}")
+        shape = positions.shape
+        if positions.dtype != torch.int32 or positions.get_device() != device or not positions.is_contiguous() or \
+                (shape != (self.axes, n) and (self.axes > 1 or shape != (n,))):
+            raise ValueError(f"positions: expected contiguous int32 [{self.axes}][{n}] on cuda:{device}, got "
+                             f"{positions.dtype} {tuple(shape)} on {positions.device}")
         for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None and (w.dtype != dtype or w.device != device or tuple(w.shape) != (self.head_dim,) or
+            if w is not None and (w.dtype != dtype or w.get_device() != device or w.shape != (self.head_dim,) or
                                   not w.is_contiguous()):
-                raise ValueError(f"{name}: expected contiguous {dtype} [{self.head_dim}] on {device}")
-        qs = ks = vs = 0
+                raise ValueError(f"{name}: expected contiguous {dtype} [{self.head_dim}] on cuda:{device}")
+        hq = hk = hv = qs = ks = vs = 0
         if q is not None:
-            qs, q_out = self._side(q, q_out, "q", n, dtype, device)
+            hq, qs, q_out = self._side(q, q_out, "q", n, dtype, device)
         if k is not None:
-            ks, k_out = self._side(k, k_out, "k", n, dtype, device)
+            hk, ks, k_out = self._side(k, k_out, "k", n, dtype, device)
         if v is not None:
-            vs, v_out = self._side(v, v_out, "v", n, dtype, device)
-        if k is not None and v is not None and k.shape[1] != v.shape[1]:
+            hv, vs, v_out = self._side(v, v_out, "v", n, dtype, device)
+        if hk and hv and hk != hv:
             raise ValueError("k and v: expected as many heads")
-        kv = k if k is not None else v
-        st = duo_qk_norm_rope(self.handle, n, 0 if q is None else q.shape[1], 0 if kv is None else kv.shape[1],
-                              _DTYPES[dtype], q, qs, k, ks, v, vs, q_weight, k_weight, eps, positions, q_out, k_out,
-                              v_out, _stream_ptr(stream))
+        stream = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_ptr(stream)
+        st = duo_qk_norm_rope(self.handle, n, hq, hk or hv, code, q, qs, k, ks, v, vs, q_weight, k_weight, eps,
+                              positions, q_out, k_out, v_out, stream)
         if st != DUO_OK:
             raise DuoError(st, "duo_qk_norm_rope")
         return q_out, k_out, v_out
