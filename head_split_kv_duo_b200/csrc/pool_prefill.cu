@@ -274,7 +274,7 @@ void deal_items(const std::vector<Item> &items, int sms, Deal *d) {
     if (u == n) return;
     int64_t rest = -static_cast<int64_t>(t0) * items[u].tile_cost;
     for (int i = u; i < n; ++i) rest += cost(i);
-    even += std::max<int64_t>(1, rest / ctas);
+    even += std::max<int64_t>({1, rest / ctas, even / 128});
   }
 }
 

@@ -151,7 +151,7 @@ def deal(items, sms):
             rank += got > 0
         if u == n:
             return whole, ctas, shares, cuts
-        even += max(1, (sum(cost[u:]) - t0 * items[u][1]) // ctas)
+        even += max(1, (sum(cost[u:]) - t0 * items[u][1]) // ctas, even // 128)
 
 
 def test_dealing_covers_every_tile_once():
