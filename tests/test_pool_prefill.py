@@ -441,6 +441,72 @@ def test_prefill_on_another_stream_and_captured(mask, replays):
 
 
 @pytest.mark.gpu
+def test_calls_back_to_back():
+    """Norms, pre-fills, forks, decodes and copies right behind one another (each launch's
+    start overlaps the one before) give what they give with a wait after every call."""
+    Hq, Hkv, mask = 16, 4, [1, 0, 1, 0]
+
+    def run(wait):
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        pool, to = (_gpu_pool(Hq, Hkv, mask, 4, 100, max_len=8000, num_pages=300) for _ in range(2))
+        rope = DuoRope(128, freqs(128))
+        outs, seqs = [], [pool.open() for _ in range(3)]
+        for step in range(6):
+            n = [700 + 150 * step, 130, 5 + step]
+            x = inputs.randn((sum(n), Hq + 2 * Hkv, 128), 9100 + step, device=DEV)
+            q, k, v = x.split((Hq, Hkv, Hkv), 1)
+            pos = torch.arange(sum(n), dtype=torch.int32, device=DEV)
+            done()
+            q, k, v = rope.norm_rope(q, k, pos, v=v)
+            done()
+            outs += pool.prefill(0, seqs, n, q, k, v)
+            done()
+            kids = pool.fork(seqs[step % 3], 2)
+            done()
+            q, k, v = (inputs.randn((1, 5, h, 128), 9200 + 10 * step + i, device=DEV)
+                       for i, h in enumerate((Hq, Hkv, Hkv)))
+            done()
+            outs += pool.decode_step(0, 1, seqs + kids, q, k, v)
+            done()
+            moved = pool.copy(kids[0], to)
+            done()
+            outs += to.prefill(0, [moved], [5], *(t[0] for t in (q, k, v)))
+            done()
+            outs += pool.decode_step(0, 1, kids, *(t[:, :2].contiguous() for t in (q, k, v)))
+            done()
+            for c in kids:
+                pool.close_seq(c)
+        assert pool.device_status() == 0 and to.device_status() == 0
+        return [t.clone() for t in outs]
+
+    waited = run(True)
+    for _ in range(3):
+        for i, (a, b) in enumerate(zip(run(False), waited)):
+            assert torch.equal(a, b), f"output {i} differs"
+
+
+@pytest.mark.gpu
+def test_two_pools_on_two_streams():
+    """Calls on two pools at the same time, each on a stream of its own."""
+    made = [Tokens(_gpu_pool(16, 4, [1, 0, 1, 0], 4, 100, max_len=9000, num_pages=200), 9500 + i) for i in range(2)]
+    x = [[t.draw(400, h) for h in (16, 4, 4)] for t in made]
+    seqs = [t.open(3000 + 500 * i) for i, t in enumerate(made)]
+    alone, kids = [], []
+    for t, s, (q, k, v) in zip(made, seqs, x):
+        kids.append(t.pool.fork(s, 4))
+        alone.append(t.pool.prefill(0, kids[-1][:1], [400], q, k, v))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in made], [[], []]
+    for j in range(1, 4):
+        for i, t in enumerate(made):
+            got[i].append(t.pool.prefill(0, kids[i][j:j + 1], [400], *x[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for want, rows in zip(alone, got):
+        for out, lse in rows:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
 def test_prefill_repeats_bit_for_bit():
     """The same call on forks of the same sequence gives the same bits, alone or beside
     others (the split may differ then: alone twice), and whatever a neighbour holds."""
