@@ -478,7 +478,7 @@ duo_status duo_pool_append_kv(duo_pool *P, int layer, int seq, const void *k, co
       // earlier pieces are in the cache: the length follows them (the contract: len
       // describes what the cache holds)
       P->len[seq][layer] = len + t0;
-      while (static_cast<int64_t>(pg.size()) > (len + t0 + kPoolTile - 1) / kPoolTile) {
+      while (static_cast<int64_t>(pg.size()) > std::max(have, (len + t0 + kPoolTile - 1) / kPoolTile)) {
         P->drop_page(pg.back());
         pg.pop_back();
       }

@@ -190,6 +190,24 @@ def test_pages_come_lowest_first(dry_run):
     duo.duo_pool_destroy(h)
 
 
+def test_append_that_fails_on_the_way_keeps_the_other_layers_pages(dry_run):
+    """An append of several launches whose second one fails: the pages that another, longer
+    layer holds -- shared ones among them -- stay listed."""
+    h = _pool(max_len=100000, num_pages=1200)
+    s = duo.duo_pool_open(h)[1]
+    _fill(h, s, [70000, 0])
+    before, free = _listed(h, s), _free(h)
+    assert len(before) == 547
+    append = lambda seq, n: duo.duo_pool_append_kv(h, 1, seq, FAKE, FAKE, n)  # noqa: E731
+    assert _fail(1, lambda: append(s, 40000)) == duo.DUO_ERR_CUDA
+    assert duo.duo_pool_len(h, s, 1)[1] == 32512 and duo.duo_pool_len(h, s, 0)[1] == 70000
+    assert _listed(h, s) == before and _free(h) == free
+    # past the longer layer: only what the call itself took goes back
+    assert _fail(1, lambda: append(s, 50000)) == duo.DUO_ERR_CUDA
+    assert duo.duo_pool_len(h, s, 1)[1] == 65024 and _listed(h, s) == before and _free(h) == free
+    duo.duo_pool_destroy(h)
+
+
 # ---------------------------------------------------------------- on the GPU
 
 def _tokens(layers, T, Hkv, seed):
