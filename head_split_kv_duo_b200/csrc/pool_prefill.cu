@@ -19,33 +19,41 @@ namespace {
 // An item whose key tiles several CTAs share: its query rows and the places of its pieces
 // in the scratch, part0, part1, part1 + 2, ...
 struct PrefillCut {
-  int seq, block, head, pieces, part0, part1;
+  int n, tok0;  // of its sequence
+  int block, head, pieces, part0, part1;
   int join0;  // blocks of the last launch that join cuts before it
 };
+struct FinishSeq {
+  int slot, len, n, tok0;
+  int page0;  // its entries in `pages`, from logical page len / 128 on
+  int unused[3];
+};
 
-// The call's last launch, sequences in the caller's order.
+// The call's last launch, sequences in the caller's order (and one that starts where the
+// last ends).  What belongs together lies together: a short launch waits for the first
+// touch of every line of its parameters.
 struct PoolFinishCall {
-  const PoolLayerDesc *layer;
+  const HeadMap *hm;  // device
+  char *rk, *rv, *sk, *sv;
   int *table;
   int pages_per_seq;
   const char *k, *v;
   char *out;
   float *lse;
   const float *partials;
-  int nseq, tokens, Hq, Hkv, G, S, W, npos, npages, ncuts, join_blocks;
-  int slot[kPoolMaxSeqs], len[kPoolMaxSeqs], n[kPoolMaxSeqs];
-  int tok0[kPoolMaxSeqs + 1];
-  int page0[kPoolMaxSeqs + 1];  // a sequence's entries in `pages`, from logical page len / 128 on
+  int nseq, tokens, Hq, Hkv, Hr, Hs, G, S, W, npos, npages, ncuts, join_blocks;
+  FinishSeq seq[kPoolMaxSeqs + 1];
   PrefillCut cuts[kPrefillCtas];
   int pages[kPrefillMaxPages];
 };
 
-// index of the last entry of first[0 .. n) that is <= x (first[0] <= x)
-__device__ __forceinline__ int find(const int *first, int n, int x) {
-  int lo = 0, hi = n - 1;
+// the last sequence with first <= x, of those where `first` is its tok0 or page0
+template <int FinishSeq::*kFirst>
+__device__ __forceinline__ int find(const PoolFinishCall &c, int x) {
+  int lo = 0, hi = c.nseq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= x) lo = mid;
+    if (c.seq[mid].*kFirst <= x) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -69,7 +77,7 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
   const int local = block - cut.join0, group = local % kJoinGroups * 2, thread = threadIdx.x / rows;
   const int r = local / kJoinGroups * rows + threadIdx.x % rows, tile = r / 128, row = r % 128;
   const int pos = (cut.block * 2 + tile) * c.npos + row / c.G;
-  const bool live = row < c.G * c.npos && pos < c.n[cut.seq];
+  const bool live = row < c.G * c.npos && pos < cut.n;
   if (threads == 1 && !live) return;
   auto part = [&](int i) {
     const int place = i == 0 ? cut.part0 : cut.part1 + 2 * (i - 1);
@@ -134,7 +142,7 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
     }
   }
   const float inv = 1.f / l;
-  const int64_t out = static_cast<int64_t>(c.tok0[cut.seq] + pos) * c.Hq + cut.head * c.G + row % c.G;
+  const int64_t out = static_cast<int64_t>(cut.tok0 + pos) * c.Hq + cut.head * c.G + row % c.G;
   uint32_t b16[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -154,53 +162,55 @@ __global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_c
   if (static_cast<int>(blockIdx.x) < c.join_blocks) return join_rows(c, blockIdx.x);
   int64_t w = (static_cast<int64_t>(blockIdx.x - c.join_blocks) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  const PoolLayerDesc &L = *c.layer;
   const int64_t append = static_cast<int64_t>((c.tokens + kAppendTokens - 1) / kAppendTokens) * c.Hkv;
   if (w < append) {
-    const int t0 = static_cast<int>(w / c.Hkv) * kAppendTokens, g = static_cast<int>(w % c.Hkv), idx = L.hm.kind_idx[g];
-    const bool is_k = lane < 16, retr = L.hm.is_retr[g];
+    const int t0 = static_cast<int>(w / c.Hkv) * kAppendTokens, g = static_cast<int>(w % c.Hkv);
+    const int idx = c.hm->kind_idx[g];
+    const bool is_k = lane < 16, retr = c.hm->is_retr[g];
     const char *src = (is_k ? c.k : c.v) + (static_cast<int64_t>(t0) * c.Hkv + g) * 256 + (lane & 15) * 16;
-    char *base = retr ? (is_k ? L.rk : L.rv) : (is_k ? L.sk : L.sv);
+    char *base = retr ? (is_k ? c.rk : c.rv) : (is_k ? c.sk : c.sv);
     uint4 x[kAppendTokens];
 #pragma unroll
     for (int i = 0; i < kAppendTokens; ++i)
       if (t0 + i < c.tokens) x[i] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(i) * c.Hkv * 256));
-    int s = find(c.tok0, c.nseq, t0);
+    int s = find<&FinishSeq::tok0>(c, t0);
 #pragma unroll
     for (int i = 0; i < kAppendTokens; ++i) {
       const int t = t0 + i;
       if (t >= c.tokens) break;
-      while (t >= c.tok0[s + 1]) ++s;
-      const int pos = c.len[s] + t - c.tok0[s], end = c.len[s] + c.n[s];
+      while (t >= c.seq[s + 1].tok0) ++s;
+      const FinishSeq &q = c.seq[s];
+      const int pos = q.len + t - q.tok0, end = q.len + q.n;
       int64_t row;
       if (retr) {
-        const int page = c.pages[c.page0[s] + pos / kPoolTile - c.len[s] / kPoolTile];
-        row = (static_cast<int64_t>(page) * L.Hr + idx) * kPoolTile + pos % kPoolTile;
+        const int page = c.pages[q.page0 + pos / kPoolTile - q.len / kPoolTile];
+        row = (static_cast<int64_t>(page) * c.Hr + idx) * kPoolTile + pos % kPoolTile;
       } else {
         if (pos >= c.S && pos < end - c.W) continue;  // evicted within the call
-        row = (static_cast<int64_t>(c.slot[s]) * L.Hs + idx) * (c.S + c.W) + (pos < c.S ? pos : c.S + pos % c.W);
+        row = (static_cast<int64_t>(q.slot) * c.Hs + idx) * (c.S + c.W) + (pos < c.S ? pos : c.S + pos % c.W);
       }
       *reinterpret_cast<uint4 *>(base + row * 256 + (lane & 15) * 16) = x[i];
     }
     return;
   }
   w -= append;
-  if (w < static_cast<int64_t>(c.nseq) * L.Hr) {
-    const int s = static_cast<int>(w / L.Hr), h = static_cast<int>(w % L.Hr);
-    const int end = c.len[s] + c.n[s], last = end / kPoolTile * kPoolTile;  // first row of the page that holds `end`
-    if (end != last && last >= c.len[s]) {  // this layer opened it with this call
-      const int page = c.pages[c.page0[s + 1] - 1];
-      const int64_t at = ((static_cast<int64_t>(page) * L.Hr + h) * kPoolTile + end - last) * 256;
+  if (w < static_cast<int64_t>(c.nseq) * c.Hr) {
+    const int s = static_cast<int>(w / c.Hr), h = static_cast<int>(w % c.Hr);
+    const FinishSeq &q = c.seq[s];
+    const int end = q.len + q.n, last = end / kPoolTile * kPoolTile;  // first row of the page that holds `end`
+    if (end != last && last >= q.len) {  // this layer opened it with this call
+      const int page = c.pages[c.seq[s + 1].page0 - 1];
+      const int64_t at = ((static_cast<int64_t>(page) * c.Hr + h) * kPoolTile + end - last) * 256;
       for (int i = lane; i < (last + kPoolTile - end) * 16; i += 32) {
-        reinterpret_cast<uint4 *>(L.rk + at)[i] = make_uint4(0, 0, 0, 0);
-        reinterpret_cast<uint4 *>(L.rv + at)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4 *>(c.rk + at)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4 *>(c.rv + at)[i] = make_uint4(0, 0, 0, 0);
       }
     }
   }
   const int64_t i = w * 32 + lane;
   if (i < c.npages) {
-    const int s = find(c.page0, c.nseq, static_cast<int>(i));
-    c.table[static_cast<int64_t>(c.slot[s]) * c.pages_per_seq + c.len[s] / kPoolTile + i - c.page0[s]] = c.pages[i];
+    const FinishSeq &q = c.seq[find<&FinishSeq::page0>(c, static_cast<int>(i))];
+    c.table[static_cast<int64_t>(q.slot) * c.pages_per_seq + q.len / kPoolTile + i - q.page0] = c.pages[i];
   }
 }
 
@@ -320,8 +330,12 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
 
   PoolPrefillCall a{};
   PoolFinishCall f{};
-  f.layer = P->d_layers + layer;
+  f.hm = &P->d_layers[layer].hm;
   const PoolLayerDesc &desc = P->h_layers[layer];
+  f.rk = desc.rk;
+  f.rv = desc.rv;
+  f.sk = desc.sk;
+  f.sv = desc.sv;
   a.tm_kr = desc.tm_kr;
   a.tm_vr = desc.tm_vr;
   a.tm_ks = desc.tm_ks;
@@ -341,24 +355,20 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   a.G = f.G = P->G;
   a.S = f.S = P->S;
   a.W = f.W = P->W;
-  a.Hr = Hr;
-  a.Hs = Hs;
+  a.Hr = f.Hr = Hr;
+  a.Hs = f.Hs = Hs;
   a.scale_log2 = P->scale * kLog2e;
   f.tokens = static_cast<int>(tokens);
   a.npos = f.npos = prefill_tile_positions(P->G);
   f.npages = static_cast<int>(entries);
   int tok = 0, page = 0;
   for (int i = 0; i < nseq; ++i) {
-    f.slot[i] = seqs[i];
-    f.len[i] = static_cast<int>(P->len[seqs[i]][layer]);
-    f.n[i] = n[i];
-    f.tok0[i] = tok;
-    f.page0[i] = page;
+    const int len = static_cast<int>(P->len[seqs[i]][layer]);
+    f.seq[i] = {seqs[i], len, n[i], tok, page, {}};
     tok += n[i];
-    page += static_cast<int>(need[i] - f.len[i] / kPoolTile);
+    page += static_cast<int>(need[i] - len / kPoolTile);
   }
-  f.tok0[nseq] = tok;
-  f.page0[nseq] = page;
+  f.seq[nseq] = {0, 0, 0, tok, page, {}};
   std::vector<Item> items;
   for (int kind = 0; kind < 2; ++kind) {  // retrieval heads' items, then streaming heads'
     const int heads = kind == 0 ? Hr : Hs;
@@ -368,7 +378,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
       first[i + 1] = first[i] + blocks * heads;
       for (int b = blocks - 1; b >= 0 && heads > 0; --b) {
         PrefillRun runs[kPrefillMaxRuns];
-        const int k = prefill_runs(kind == 0, f.len[s], n[s], b * 2 * f.npos, f.npos, P->S, P->W, runs);
+        const int k = prefill_runs(kind == 0, f.seq[s].len, n[s], b * 2 * f.npos, f.npos, P->S, P->W, runs);
         int t = 0;
         for (int r = 0; r < k; ++r) t += runs[r].count;
         items.insert(items.end(), heads, Item{t, kind == 0 ? kTileCost : kStreamingTileCost});
@@ -377,10 +387,10 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   }
   for (int i = 0; i < nseq; ++i) {
     const int s = order[i];
-    a.lists.slot[i] = f.slot[s];
-    a.lists.len[i] = f.len[s];
-    a.lists.n[i] = f.n[s];
-    a.lists.tok0[i] = f.tok0[s];
+    a.lists.slot[i] = f.seq[s].slot;
+    a.lists.len[i] = f.seq[s].len;
+    a.lists.n[i] = f.seq[s].n;
+    a.lists.tok0[i] = f.seq[s].tok0;
     a.lists.blocks[i] = prefill_blocks(n[s], P->G);
   }
   const HeadMap &hm = desc.hm;
@@ -400,7 +410,8 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     const int *first = retr ? a.lists.rfirst : a.lists.sfirst;
     const int at = static_cast<int>(std::upper_bound(first, first + nseq, u) - first) - 1;
     const int rem = u - first[at];
-    f.cuts[i] = {order[at], prefill_blocks(n[order[at]], P->G) - 1 - rem / heads,
+    const FinishSeq &q = f.seq[order[at]];
+    f.cuts[i] = {q.n, q.tok0, prefill_blocks(q.n, P->G) - 1 - rem / heads,
                  retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1,
                  f.join_blocks};
     f.join_blocks += kJoinGroups * join_threads(cut.pieces);
@@ -414,7 +425,8 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     std::vector<int> &pg = P->pages[seqs[i]];
     have[i] = pg.size();
     while (static_cast<int64_t>(pg.size()) < need[i]) pg.push_back(P->take_page());
-    for (int e = f.page0[i]; e < f.page0[i + 1]; ++e) f.pages[e] = pg[f.len[i] / kPoolTile + e - f.page0[i]];
+    for (int e = f.seq[i].page0; e < f.seq[i + 1].page0; ++e)
+      f.pages[e] = pg[f.seq[i].len / kPoolTile + e - f.seq[i].page0];
   }
   cudaError_t e = launch_via_hook([&] { return launch_prefill_pool_tc(a, st); });
   if (e == cudaSuccess)
