@@ -43,6 +43,7 @@ struct PoolFinishCall {
   const float *partials;
   int nseq, tokens, Hq, Hkv, Hr, Hs, G, S, W, npos, npages, ncuts, join_blocks;
   FinishSeq seq[kPoolMaxSeqs + 1];
+  uint8_t cut_of[4 * kPrefillCtas];  // of each 16 blocks that join
   PrefillCut cuts[kPrefillCtas];
   int pages[kPrefillMaxPages];
 };
@@ -63,16 +64,11 @@ __device__ __forceinline__ int find(const PoolFinishCall &c, int x) {
 // loads in flight; or, of more than four pieces, of 64 of its rows, four threads per row,
 // each joining every fourth piece, and the first of them the four.
 constexpr int kJoinGroups = 128 / 8;
+static_assert(kJoinGroups == 16 && kPrefillCtas <= 256, "cut_of");
 __host__ __device__ inline int join_threads(int pieces) { return pieces > 4 ? 4 : 1; }
 __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
   __shared__ float others[3][10][64];
-  int at = 0;  // the last cut with join0 <= block
-  for (int hi = c.ncuts - 1; at < hi;) {
-    const int mid = (at + hi + 1) >> 1;
-    if (c.cuts[mid].join0 <= block) at = mid;
-    else hi = mid - 1;
-  }
-  const PrefillCut &cut = c.cuts[at];
+  const PrefillCut &cut = c.cuts[c.cut_of[block / kJoinGroups]];
   const int pieces = cut.pieces, threads = join_threads(pieces), rows = kPrefillRows / threads;
   const int local = block - cut.join0, group = local % kJoinGroups * 2, thread = threadIdx.x / rows;
   const int r = local / kJoinGroups * rows + threadIdx.x % rows, tile = r / 128, row = r % 128;
@@ -414,7 +410,8 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
     f.cuts[i] = {q.n, q.tok0, prefill_blocks(q.n, P->G) - 1 - rem / heads,
                  retr ? hm.retr_head[rem % heads] : hm.strm_head[rem % heads], cut.pieces, cut.part0, cut.part1,
                  f.join_blocks};
-    f.join_blocks += kJoinGroups * join_threads(cut.pieces);
+    for (int j = 0; j < join_threads(cut.pieces); ++j, f.join_blocks += kJoinGroups)
+      f.cut_of[f.join_blocks / kJoinGroups] = static_cast<uint8_t>(i);
   }
   if (!dry_run() && prepare_prefill_pool_tc(&a, q, k, v, f.tokens) != cudaSuccess) return DUO_ERR_CUDA;
   for (int i = 0; i < nseq; ++i) P->pages[seqs[i]].reserve(static_cast<size_t>(need[i]));
