@@ -633,11 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
         for (int q = 0; q < 4; ++q) {
           float x[32];
           tc::ld<32>(o_cols + 32 * q, x);
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            to[(8 * q + e) * kBM] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            for (int e = 0; e < 8; ++e)
+              to[(8 * q + e) * kBM] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          }
         }
-        to[(kD / 4) * kBM] = make_float4(m, l, 0.f, 0.f);
+        if (live) to[(kD / 4) * kBM] = make_float4(m, l, 0.f, 0.f);
       } else {
         const int64_t at = live ? static_cast<int64_t>(tok) * c.Hq + head : -1;
         const float inv = 1.f / l;

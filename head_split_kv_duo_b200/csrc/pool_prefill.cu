@@ -43,7 +43,7 @@ struct PoolFinishCall {
   const float *partials;
   int nseq, tokens, Hq, Hkv, Hr, Hs, G, S, W, npos, npages, ncuts, join_blocks;
   FinishSeq seq[kPoolMaxSeqs + 1];
-  uint8_t cut_of[4 * kPrefillCtas];  // of each 16 blocks that join
+  uint8_t cut_of[4 * kPrefillCtas];  // of each kJoinGroups blocks that join
   PrefillCut cuts[kPrefillCtas];
   int pages[kPrefillMaxPages];
 };
@@ -60,17 +60,18 @@ __device__ __forceinline__ int find(const PoolFinishCall &c, int x) {
   return lo;
 }
 
-// A block joins eight dimensions of a cut item's 256 rows, one thread per row, four pieces'
-// loads in flight; or, of more than four pieces, of 64 of its rows, four threads per row,
-// each joining every fourth piece, and the first of them the four.
-constexpr int kJoinGroups = 128 / 8;
-static_assert(kJoinGroups == 16 && kPrefillCtas <= 256, "cut_of");
+// A block joins sixteen dimensions of a cut item's 256 rows, one thread per row, four
+// pieces' loads in flight; or, of more than four pieces, of 64 of its rows, four threads per
+// row, each joining every fourth piece, and the first of them the four.
+constexpr int kJoinVecs = 4;  // float4 vectors of a thread
+constexpr int kJoinGroups = 32 / kJoinVecs;
+static_assert(kPrefillCtas <= 256, "cut_of");
 __host__ __device__ inline int join_threads(int pieces) { return pieces > 4 ? 4 : 1; }
 __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
-  __shared__ float others[3][10][64];
+  __shared__ float others[3][2 + 4 * kJoinVecs][64];
   const PrefillCut &cut = c.cuts[c.cut_of[block / kJoinGroups]];
   const int pieces = cut.pieces, threads = join_threads(pieces), rows = kPrefillRows / threads;
-  const int local = block - cut.join0, group = local % kJoinGroups * 2, thread = threadIdx.x / rows;
+  const int local = block - cut.join0, group = local % kJoinGroups * kJoinVecs, thread = threadIdx.x / rows;
   const int r = local / kJoinGroups * rows + threadIdx.x % rows, tile = r / 128, row = r % 128;
   const int pos = (cut.block * 2 + tile) * c.npos + row / c.G;
   const bool live = row < c.G * c.npos && pos < cut.n;
@@ -79,18 +80,19 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
     const int place = i == 0 ? cut.part0 : cut.part1 + 2 * (i - 1);
     return reinterpret_cast<const float4 *>(c.partials) + (place * 2 + tile) * (kPrefillRow / 4) * 128 + row;
   };
-  float m = -INFINITY, l = 0.f, o[8] = {};
+  float m = -INFINITY, l = 0.f, o[4 * kJoinVecs] = {};
   for (int i0 = thread; i0 < pieces && live; i0 += 4 * threads) {
-    float4 ml[4], x[4], y[4];
+    float4 ml[4], x[4][kJoinVecs];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       ml[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      x[e] = y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + e * threads < pieces) {
-        const float4 *p = part(i0 + e * threads);
-        ml[e] = p[32 * 128];
-        x[e] = p[group * 128];
-        y[e] = p[(group + 1) * 128];
+      const bool there = i0 + e * threads < pieces;
+      const float4 *p = part(there ? i0 + e * threads : i0);
+      if (there) ml[e] = p[32 * 128];
+#pragma unroll
+      for (int k = 0; k < kJoinVecs; ++k) {
+        x[e][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there) x[e][k] = p[(group + k) * 128];
       }
     }
     const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
@@ -99,19 +101,18 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
     m = top;
     l *= old;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] *= old;
+    for (int k = 0; k < 4 * kJoinVecs; ++k) o[k] *= old;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float w = ex2(ml[e].x - m);
       l = fmaf(ml[e].y, w, l);
-      o[0] = fmaf(w, x[e].x, o[0]);
-      o[1] = fmaf(w, x[e].y, o[1]);
-      o[2] = fmaf(w, x[e].z, o[2]);
-      o[3] = fmaf(w, x[e].w, o[3]);
-      o[4] = fmaf(w, y[e].x, o[4]);
-      o[5] = fmaf(w, y[e].y, o[5]);
-      o[6] = fmaf(w, y[e].z, o[6]);
-      o[7] = fmaf(w, y[e].w, o[7]);
+#pragma unroll
+      for (int k = 0; k < kJoinVecs; ++k) {
+        o[4 * k] = fmaf(w, x[e][k].x, o[4 * k]);
+        o[4 * k + 1] = fmaf(w, x[e][k].y, o[4 * k + 1]);
+        o[4 * k + 2] = fmaf(w, x[e][k].z, o[4 * k + 2]);
+        o[4 * k + 3] = fmaf(w, x[e][k].w, o[4 * k + 3]);
+      }
     }
   }
   if (threads > 1) {
@@ -121,7 +122,7 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
       to[0] = m;
       to[64] = l;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) to[64 * (2 + k)] = o[k];
+      for (int k = 0; k < 4 * kJoinVecs; ++k) to[64 * (2 + k)] = o[k];
     }
     __syncthreads();
     if (thread > 0 || !live) return;
@@ -134,18 +135,21 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
       m = top;
       l = l * a + from[64] * b;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = o[k] * a + from[64 * (2 + k)] * b;
+      for (int k = 0; k < 4 * kJoinVecs; ++k) o[k] = o[k] * a + from[64 * (2 + k)] * b;
     }
   }
   const float inv = 1.f / l;
   const int64_t out = static_cast<int64_t>(cut.tok0 + pos) * c.Hq + cut.head * c.G + row % c.G;
-  uint32_t b16[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-    b16[e] = *reinterpret_cast<const uint32_t *>(&b);
+  for (int k = 0; k < kJoinVecs / 2; ++k) {
+    uint32_t b16[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
+      b16[e] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(c.out + out * 256 + group * 8 + k * 16) = make_uint4(b16[0], b16[1], b16[2], b16[3]);
   }
-  *reinterpret_cast<uint4 *>(c.out + out * 256 + group * 8) = make_uint4(b16[0], b16[1], b16[2], b16[3]);
   if (group == 0 && c.lse) c.lse[out] = (m + lg2(l)) * kLn2;
 }
 
