@@ -60,10 +60,12 @@ __device__ __forceinline__ int find(const PoolFinishCall &c, int x) {
   return lo;
 }
 
-// A block joins sixteen dimensions of a cut item's 256 rows, one thread per row, four
-// pieces' loads in flight; or, of more than four pieces, of 64 of its rows, four threads per
-// row, each joining every fourth piece, and the first of them the four.
-constexpr int kJoinVecs = 4;  // float4 vectors of a thread
+// A block joins sixteen dimensions of a cut item's 256 rows, one thread per row, two pieces'
+// loads in flight (three blocks an SM; with four in flight, two); or, of more than four
+// pieces, of 64 of its rows, four threads per row, each joining every fourth piece, and the
+// first of them the four.
+constexpr int kJoinVecs = 4;   // float4 vectors of a thread
+constexpr int kJoinAhead = 2;  // pieces whose loads are in flight
 constexpr int kJoinGroups = 32 / kJoinVecs;
 static_assert(kPrefillCtas <= 256, "cut_of");
 __host__ __device__ inline int join_threads(int pieces) { return pieces > 4 ? 4 : 1; }
@@ -81,10 +83,10 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
     return reinterpret_cast<const float4 *>(c.partials) + (place * 2 + tile) * (kPrefillRow / 4) * 128 + row;
   };
   float m = -INFINITY, l = 0.f, o[4 * kJoinVecs] = {};
-  for (int i0 = thread; i0 < pieces && live; i0 += 4 * threads) {
-    float4 ml[4], x[4][kJoinVecs];
+  for (int i0 = thread; i0 < pieces && live; i0 += kJoinAhead * threads) {
+    float4 ml[kJoinAhead], x[kJoinAhead][kJoinVecs];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kJoinAhead; ++e) {
       ml[e] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
       const bool there = i0 + e * threads < pieces;
       const float4 *p = part(there ? i0 + e * threads : i0);
@@ -95,7 +97,9 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
         if (there) x[e][k] = p[(group + k) * 128];
       }
     }
-    const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+    float top = m;
+#pragma unroll
+    for (int e = 0; e < kJoinAhead; ++e) top = fmaxf(top, ml[e].x);
     if (top == -INFINITY) continue;  // the row saw nothing so far
     const float old = ex2(m - top);  // 0 while m is -inf
     m = top;
@@ -103,7 +107,7 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
 #pragma unroll
     for (int k = 0; k < 4 * kJoinVecs; ++k) o[k] *= old;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kJoinAhead; ++e) {
       const float w = ex2(ml[e].x - m);
       l = fmaf(ml[e].y, w, l);
 #pragma unroll
@@ -157,7 +161,7 @@ __device__ __forceinline__ void join_rows(const PoolFinishCall &c, int block) {
 // lower lanes, V on the upper; then one per (sequence, retrieval head) for the rest of a
 // page that the call opened, and the block-table entries.
 constexpr int kAppendTokens = 8;
-__global__ void __launch_bounds__(256) pool_prefill_finish_kernel(const __grid_constant__ PoolFinishCall c) {
+__global__ void __launch_bounds__(256, 3) pool_prefill_finish_kernel(const __grid_constant__ PoolFinishCall c) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (static_cast<int>(blockIdx.x) < c.join_blocks) return join_rows(c, blockIdx.x);
   int64_t w = (static_cast<int64_t>(blockIdx.x - c.join_blocks) * blockDim.x + threadIdx.x) >> 5;
