@@ -40,8 +40,8 @@
 // many of MUFU (exponentials of two warps per scheduler); it takes about 2650, and long
 // calls run at the power limit (1.66 GHz).  8 KV heads (4 of them retrieval heads) of 4
 // query heads, alone on the GPU with the append:
-//   8192 tokens on 24576: 1.51 ms, 1.30 PFLOP/s (back to back, at 1.45 GHz, 1.75 ms)
-//   64 tokens on 131000: 73 us (0.27 GB and 69 GFLOP: 41 us at either rate)
+//   8192 tokens on 24576: 1.51 ms, 1.30 PFLOP/s (back to back, at 1.45 GHz, 1.71 ms)
+//   64 tokens on 131000: 72 us with a fork (0.27 GB and 69 GFLOP: 41 us at either rate)
 // Steps from a first version of 1.89 ms and 84 us (one CTA per item, the maximum before the
 // exponentials, P handed over whole, lane 0 alone issuing), in that order:
 //   products of a tile's first 96 keys start before the other 32 are done, the maximum is
@@ -50,7 +50,7 @@
 //   rows out through shared memory, partial rows transposed, masks as two runs: 1.55 ms
 //   one site each for listing and storing (84 -> 75 KB of code: the loops then stay in the
 //   instruction cache): 1.51 ms
-//   even shares by cost: 630 -> 340 us for eight sequences of very different lengths
+//   even shares by cost: 630 -> 330 us for eight sequences of very different lengths
 // Without gain: part of the exponentials as polynomials on the FMA pipe (1.55 to 1.76 ms for
 // an eighth to a third of them), P in halves (1.65) or whole (1.54), tiles fetched into L2
 // ahead of their loads (73 -> 85 us), listing pieces with a function call.
