@@ -5,6 +5,10 @@
 // A row whose keys were cut into pieces with partial sums O_s, maxima m_s (base 2) and
 // weights l_s is O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, M = max m_s, lse = (M +
 // log2 of the denominator) ln 2; pieces in order, so a result does not depend on timing.
+//
+// The last launch is bound by latency when it is short (4 to 5 us: parameters, partial
+// rows, stores, one after the other) and by the partial rows otherwise: 8192 tokens on
+// 24576, 40 MB of them and 33 MB of k and v in, 17 MB of rows out, 18 us.
 #include <cmath>
 #include <exception>
 
