@@ -113,10 +113,10 @@ def test_streaming_tiles_cover_what_is_visible():
 def deal(items, sms):
     """The host's dealing of items [(tiles, cost of one)]: (whole, ctas, shares, cuts), a share
     (item, tile, tiles, part) per CTA, a cut (item, pieces, part0, part1)."""
-    piece, least, share_tiles = 16, 2, 2
+    piece = 16
     cost = [t * c + piece for t, c in items]
     n, tiles = len(items), sum(t for t, _ in items)
-    ctas = min(sms, 148, max(1, tiles // share_tiles))
+    ctas = min(sms, 148, tiles)
     even = -(-sum(cost) // ctas)
     while True:
         load, u = [0] * ctas, 0
@@ -132,11 +132,9 @@ def deal(items, sms):
             while u < n:
                 rest = items[u][0] - t0
                 can = int((room - piece) / items[u][1])  # towards zero
-                if can < min(rest, least):
+                if can < 1:
                     break
                 take = min(rest, can)
-                if rest - take < least:
-                    take = rest
                 if t0 > 0:
                     cuts[-1][1] += 1
                 elif take < rest:
