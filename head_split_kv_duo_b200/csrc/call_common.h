@@ -6,6 +6,9 @@
 
 namespace duo {
 
+// Is the test control duo_debug_device_stall on?
+bool device_stall();
+
 // A byte range of a call's tensors, for its overlap check.
 struct Span {
   uintptr_t lo, hi;

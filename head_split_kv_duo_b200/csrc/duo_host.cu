@@ -5,6 +5,7 @@
 #include <cstring>
 #include <new>
 
+#include "call_common.h"
 #include "duo_internal.h"
 #include "nvtx_range.h"
 
@@ -665,5 +666,7 @@ bool launch_intercepted(cudaError_t *e) {
   }
   return false;
 }
+
+bool device_stall() { return g_device_stall.load(std::memory_order_relaxed) != 0; }
 
 }  // namespace duo

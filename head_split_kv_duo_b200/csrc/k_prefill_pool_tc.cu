@@ -80,7 +80,7 @@ constexpr int kPFirst = 96;  // keys of a tile whose P is handed over first
 constexpr int kBarQ = 0, kBarQEmpty = 1, kBarKFull = 2, kBarKEmpty = kBarKFull + kKStages,
               kBarVFull = kBarKEmpty + kKStages, kBarVEmpty = kBarVFull + kVStages, kBarSFull = kBarVEmpty + kVStages,
               kBarPFull = kBarSFull + kQT, kBarPRest = kBarPFull + kQT, kBarOFull = kBarPRest + kQT,
-              kBarPiece = kBarOFull + kQT, kBarPieceFree = kBarPiece + kPieces, kBarDrain = kBarPieceFree + kPieces, kNumBars = kBarDrain + 1;
+              kBarPiece = kBarOFull + kQT, kBarPieceFree = kBarPiece + kPieces, kBarDrain = kBarPieceFree + kPieces, kBarStall = kBarDrain + 1, kNumBars = kBarStall + 1;
 static_assert(kNumBars * 8 <= 256 && kSmemAlloc <= 227 * 1024, "shared memory");
 
 // True in one lane of a converged warp, the same one every time.
@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
           next = {run->src, run->first * kBN};
         }
 
+        if (c.debug_stall && p == 0 && j == 0 && ok) ok = tc::wait_bar(bar(kBarStall), 0, c.status, abort_flag);
         if (ok) ok = tc::wait_bar(bar(kBarSFull + qt), s_tile & 1, c.status, abort_flag);
         ++s_tile;
         tc::fence_after();

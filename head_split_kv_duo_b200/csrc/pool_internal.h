@@ -148,6 +148,7 @@ struct PoolPrefillCall {
   uint32_t *status;
   int nseq, Hq, Hkv, G, npos, S, W, Hr, Hs, retr_items, whole_items, ctas;  // npos: positions of a query tile
   float scale_log2;
+  int debug_stall;  // test control: the softmax first waits for a barrier that nothing arrives at
   PrefillLists lists;
 };
 // Positions per query tile and items (of two tiles) that cover n positions of one KV head.

@@ -363,6 +363,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   a.Hr = f.Hr = Hr;
   a.Hs = f.Hs = Hs;
   a.scale_log2 = P->scale * kLog2e;
+  a.debug_stall = device_stall();
   f.tokens = static_cast<int>(tokens);
   a.npos = f.npos = prefill_tile_positions(P->G);
   f.npages = static_cast<int>(entries);

@@ -2,6 +2,8 @@
 kernel restated and checked on the CPU, refusals and bookkeeping with launches skipped, and
 on the GPU outputs against the fp64 oracle over each sequence's own tokens, with the cached
 rows bit for bit."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -436,6 +438,31 @@ def test_prefill_on_another_stream_and_captured(mask, replays):
         tk.kv[x][0] = (torch.cat((kk, k)), torch.cat((vv, v)))
     tk.check_cache()
     assert tk.pool.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_prefill_wait_runs_out_and_the_pool_goes_on():
+    """A pre-fill whose softmax waits for what never comes reports the timeout after about the
+    wait limit, frees what it holds, and the pool's other sequences go on as before."""
+    tk = Tokens(_gpu_pool(32, 8, [1, 0, 1, 0, 0, 1, 1, 0], 16, 512, max_len=9000, num_pages=300), 9700)
+    s, t = tk.open(3000), tk.open(100)
+    (c,) = tk.pool.fork(s)
+    q, k, v = tk.draw(900, 32), tk.draw(900, 8), tk.draw(900, 8)
+    assert tk.pool.device_status() == duo.DUO_OK
+    assert duo.duo_debug_device_stall(1) == duo.DUO_OK
+    try:
+        t0 = time.perf_counter()
+        tk.pool.prefill(0, [c], [900], q, k, v)
+        status = tk.pool.device_status()
+        seconds = time.perf_counter() - t0
+    finally:
+        assert duo.duo_debug_device_stall(0) == duo.DUO_OK
+    assert status == duo.DUO_ERR_TIMEOUT and 1.0 < seconds < 60.0, (status, seconds)
+    assert tk.pool.device_status() == duo.DUO_OK
+    tk.pool.close_seq(c)
+    tk.prefill(0, [t, s], [700, 900], rows=8)
+    tk.check_cache()
+    assert tk.pool.device_status() == duo.DUO_OK
 
 
 @pytest.mark.gpu
