@@ -1,5 +1,5 @@
-// call_common.h -- what the calls with overlap checks and overlapped launches share
-// (k_norm_rope.cu, pool_share.cu, pool_prefill.cu, k_prefill_pool_tc.cu).
+// call_common.h -- overlap checks, overlapped launches and the stall control, for the calls
+// on norms and pools (k_norm_rope.cu, pool_share.cu, pool_prefill.cu, k_prefill_pool_tc.cu).
 #pragma once
 
 #include "duo_internal.h"

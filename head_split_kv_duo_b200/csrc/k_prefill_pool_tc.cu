@@ -14,8 +14,8 @@
 // An item is two 128-row query tiles of one (sequence, KV head) -- a row is one of G query
 // heads at one of 128 / G consecutive positions (rows past G * (128 / G) idle) -- sharing
 // every K/V tile.  The grid is one CTA per SM; a CTA works through whole items and then
-// through its share of the last ones, which are cut by key tiles so that every CTA gets
-// the same number of them (few queries over a long history are nothing but that share).
+// through its share of the last ones, which are cut by key tiles so that every CTA has as
+// much to do (few queries over a long history are nothing but that share).
 // A cut item's CTAs leave unnormalised rows, max and sum in the scratch; the append launch
 // that follows joins them.  12 warps:
 //   warp 0      TMA: the K ring (2 stages)
