@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
             for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * a);
             tc::st16(o_cols + 16 * q, u);
           }
+          tc::st_wait();  // stores are in no order: the first weights land before the second are stored over them
         }
         tc::st_wait();
         tc::fence_before();
