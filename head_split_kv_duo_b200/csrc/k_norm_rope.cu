@@ -268,6 +268,26 @@ cudaError_t launch_norm_rope(NormRopeParams p, cudaStream_t st) {
   return launch_overlapped(kernel, blocks, kNrThreads, 0, st, p);
 }
 
+// The fraction of f / 2 pi, 0 <= f <= 2^20, in units of 2^-64, to the nearest: off by at most
+// 2^-65 turns, and by 2^-34 turns times any position.  f = m 2^e exactly with a 53-bit m, so
+// it is the product of m and the first 128 bits of 1 / 2 pi (at most 2^-108 turns off), an
+// integer of three words, shifted; whole turns fall off at the top.  (A quotient in
+// floating point loses as many bits of the fraction as there are whole turns per position:
+// with 64 bits and f near 10^6, 2^-47 turns, and 1.3e-4 rad at position 2^31.)
+uint64_t turn_fraction(double f) {
+  constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // floor(2^128 / 2 pi)
+  int e;
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(f, &e), 53));
+  const int s = 64 - (e - 53);  // f / 2 pi in units of 2^-64: m (2^128 / 2 pi) 2^-s; e <= 20, so s >= 97
+  using u128 = unsigned __int128;
+  const u128 lo = static_cast<u128>(m) * kLo, hi = static_cast<u128>(m) * kHi + static_cast<uint64_t>(lo >> 64);
+  const uint64_t w[4] = {static_cast<uint64_t>(lo), static_cast<uint64_t>(hi), static_cast<uint64_t>(hi >> 64), 0};
+  const int at = (s - 1) / 64, bit = (s - 1) % 64;  // the highest bit that falls off rounds
+  if (at > 2) return 0;
+  const u128 x = (static_cast<u128>(w[at + 1]) << 64 | w[at]) >> bit;  // that bit and, behind it, 64 or more
+  return static_cast<uint64_t>((x >> 1) + (x & 1));
+}
+
 }  // namespace
 
 }  // namespace duo
@@ -294,10 +314,7 @@ duo_status duo_rope_create(int head_dim, int rot_dim, const double *inv_freq, co
   r->interleaved = interleaved;
   r->scale = scale;
   for (int i = 0; i < rot_dim / 2; ++i) {
-    // 64 significant bits: |position| < 2^31 leaves the angle better than 2^-31 turns
-    const long double turns = static_cast<long double>(inv_freq[i]) / 6.283185307179586476925286766559L;
-    const long double f = turns - std::floor(turns);
-    r->freq[i] = static_cast<uint64_t>(f * 0x1p64L);
+    r->freq[i] = turn_fraction(inv_freq[i]);
     r->axis[i] = pair_axis ? pair_axis[i] : 0;
   }
   *out = r;
