@@ -15,7 +15,7 @@
 // over every (layer, sequence, KV head) item).
 #include <cmath>
 #include <cstring>
-#include <new>
+#include <memory>
 
 #include "decode_merge.cuh"
 #include "tcgen05.cuh"
@@ -269,27 +269,10 @@ namespace {
 
 bool seq_ok(const duo_pool *P, int seq) { return P && P->is_open(seq); }
 
-}  // namespace
-
-extern "C" {
-
-size_t duo_pool_bytes(int layers, int kv_heads, int head_dim, const uint8_t *mask, int S, int W, int max_seqs,
-                      int64_t max_len, int64_t num_pages, const duo_opts *opts) {
-  int Hq = 0;
-  float scale = 0.f;
-  if (pool_args(layers, kv_heads, head_dim, mask, S, W, max_seqs, max_len, num_pages, opts, &Hq, &scale) != DUO_OK)
-    return 0;
-  PoolLayout L;
-  if (!pool_layout(layers, kv_heads, Hq, mask, S, W, max_seqs, max_len, num_pages, &L)) return 0;
-  return L.total;
-}
-
-duo_status duo_pool_create(int layers, int kv_heads, int head_dim, const uint8_t *mask, int S, int W, int max_seqs,
-                           int64_t max_len, int64_t num_pages, const duo_opts *opts, void *dev_buf, size_t dev_bytes,
-                           duo_pool **out) {
-  DUO_NVTX_RANGE("duo_pool_create");
-  if (!out) return DUO_ERR_INVALID;
-  *out = nullptr;
+// duo_pool_create behind its guard against exceptions
+duo_status create_pool(int layers, int kv_heads, int head_dim, const uint8_t *mask, int S, int W, int max_seqs,
+                       int64_t max_len, int64_t num_pages, const duo_opts *opts, void *dev_buf, size_t dev_bytes,
+                       duo_pool **out) {
   int Hq = 0;
   float scale = 0.f;
   duo_status st = pool_args(layers, kv_heads, head_dim, mask, S, W, max_seqs, max_len, num_pages, opts, &Hq, &scale);
@@ -297,8 +280,7 @@ duo_status duo_pool_create(int layers, int kv_heads, int head_dim, const uint8_t
   PoolLayout L;
   if (!pool_layout(layers, kv_heads, Hq, mask, S, W, max_seqs, max_len, num_pages, &L)) return DUO_ERR_INVALID;
   if (!dev_buf || (reinterpret_cast<uintptr_t>(dev_buf) & 255u) || dev_bytes < L.total) return DUO_ERR_INVALID;
-  duo_pool *P = new (std::nothrow) duo_pool();
-  if (!P) return DUO_ERR_INVALID;
+  std::unique_ptr<duo_pool> P(new duo_pool());
   P->layers = layers;
   P->Hkv = kv_heads;
   P->Hq = Hq;
@@ -347,8 +329,41 @@ duo_status duo_pool_create(int layers, int kv_heads, int head_dim, const uint8_t
   P->open.assign(max_seqs, 0);
   P->pages.assign(max_seqs, {});
   P->len.assign(max_seqs, std::vector<int64_t>(layers, 0));
-  *out = P;
+  *out = P.release();
   return DUO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t duo_pool_bytes(int layers, int kv_heads, int head_dim, const uint8_t *mask, int S, int W, int max_seqs,
+                      int64_t max_len, int64_t num_pages, const duo_opts *opts) {
+  int Hq = 0;
+  float scale = 0.f;
+  if (pool_args(layers, kv_heads, head_dim, mask, S, W, max_seqs, max_len, num_pages, opts, &Hq, &scale) != DUO_OK)
+    return 0;
+  try {
+    PoolLayout L;
+    if (!pool_layout(layers, kv_heads, Hq, mask, S, W, max_seqs, max_len, num_pages, &L)) return 0;
+    return L.total;
+  } catch (const std::exception &) {  // out of host memory
+    return 0;
+  }
+}
+
+duo_status duo_pool_create(int layers, int kv_heads, int head_dim, const uint8_t *mask, int S, int W, int max_seqs,
+                           int64_t max_len, int64_t num_pages, const duo_opts *opts, void *dev_buf, size_t dev_bytes,
+                           duo_pool **out) {
+  DUO_NVTX_RANGE("duo_pool_create");
+  if (!out) return DUO_ERR_INVALID;
+  *out = nullptr;
+  try {
+    return create_pool(layers, kv_heads, head_dim, mask, S, W, max_seqs, max_len, num_pages, opts, dev_buf, dev_bytes,
+                       out);
+  } catch (const std::exception &) {  // out of host memory
+    return DUO_ERR_INVALID;
+  }
 }
 
 void duo_pool_destroy(duo_pool *pool) { delete pool; }
@@ -441,6 +456,11 @@ duo_status duo_pool_append_kv(duo_pool *P, int layer, int seq, const void *k, co
   if (r != DUO_OK) return r;
   // pages opened by this call come off the free pages; they go back if a launch fails
   std::vector<int> &pg = P->pages[seq];
+  try {
+    duo_pool::make_room(pg, static_cast<size_t>(std::max(have, need)));
+  } catch (const std::exception &) {  // out of host memory, before anything was taken
+    return DUO_ERR_INVALID;
+  }
   for (int64_t i = have; i < need; ++i) pg.push_back(P->take_page());
   auto undo = [&] {
     while (static_cast<int64_t>(pg.size()) > have) {
@@ -500,7 +520,14 @@ duo_status duo_pool_decode_step(duo_pool *P, int layer0, int nlayers, int nseq, 
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return DUO_ERR_INVALID;
   if (nlayers * nseq * P->Hkv > P->max_items) return DUO_ERR_CAPACITY;
-  std::vector<uint8_t> seen(P->max_seqs, 0);
+  std::vector<uint8_t> seen;
+  std::vector<int> opened;
+  try {
+    seen.assign(P->max_seqs, 0);
+    opened.reserve(nseq);
+  } catch (const std::exception &) {  // out of host memory
+    return DUO_ERR_INVALID;
+  }
   int new_pages = 0;
   for (int i = 0; i < nseq; ++i) {
     const int s = seqs[i];
@@ -516,6 +543,11 @@ duo_status duo_pool_decode_step(duo_pool *P, int layer0, int nlayers, int nseq, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   duo_status r = pool_init(P, st);
   if (r != DUO_OK) return r;
+  try {
+    for (int i = 0; i < nseq; ++i) duo_pool::make_room(P->pages[seqs[i]], P->len[seqs[i]][layer0] / kPoolTile + 1);
+  } catch (const std::exception &) {  // before anything was taken
+    return DUO_ERR_INVALID;
+  }
 
   PoolAppendCall ac{};
   ac.layers = P->d_layers;
@@ -537,7 +569,6 @@ duo_status duo_pool_decode_step(duo_pool *P, int layer0, int nlayers, int nseq, 
   dc.layer0 = layer0;
   dc.nlayers = nlayers;
   dc.nseq = nseq;
-  std::vector<int> opened;
   for (int i = 0; i < nseq; ++i) {
     const int s = seqs[i];
     const int64_t len = P->len[s][layer0];

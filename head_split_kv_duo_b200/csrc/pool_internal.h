@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <exception>
 #include <functional>
 #include <vector>
 
@@ -43,6 +44,11 @@ struct duo_pool {
     if (--refs[pg] > 0) return;
     free_pages.push_back(pg);  // within the capacity reserved at creation
     std::push_heap(free_pages.begin(), free_pages.end(), std::greater<int>());
+  }
+  // Room for `n` pages in a sequence's list (twice what it had at least, so that lists which
+  // grow page by page are moved rarely).  May throw; take_page and push_back then do not.
+  static void make_room(std::vector<int> &list, size_t n) {
+    if (list.capacity() < n) list.reserve(std::max(n, 2 * list.capacity()));
   }
   bool is_open(int seq) const { return seq >= 0 && seq < max_seqs && open[seq]; }
 };

@@ -424,7 +424,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
       f.cut_of[f.join_blocks / kJoinGroups] = static_cast<uint8_t>(i);
   }
   if (!dry_run() && prepare_prefill_pool_tc(&a, q, k, v, f.tokens) != cudaSuccess) return DUO_ERR_CUDA;
-  for (int i = 0; i < nseq; ++i) P->pages[seqs[i]].reserve(static_cast<size_t>(need[i]));
+  for (int i = 0; i < nseq; ++i) duo_pool::make_room(P->pages[seqs[i]], static_cast<size_t>(need[i]));
 
   // from here on nothing throws; pages that the call opens go back if a launch fails
   std::vector<size_t> have(nseq);
