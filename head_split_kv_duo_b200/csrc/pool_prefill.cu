@@ -474,3 +474,57 @@ extern "C" duo_status duo_pool_prefill(duo_pool *P, int layer, int nseq, const i
     return DUO_ERR_INVALID;
   }
 }
+
+extern "C" duo_status duo_debug_prefill_runs(int retrieval, int len, int n, int r0, int npos, int S, int W,
+                                             int (*runs)[3], int *nruns, int ring[4]) {
+  if ((retrieval != 0 && retrieval != 1) || len < 0 || n < 1 || r0 < 0 || r0 >= n || npos < 1 || npos > 128 ||
+      S < 0 || S > (1 << 24) || W < 1 || W > (1 << 24) || n > (1 << 30) || len > (1 << 30) || !runs || !nruns || !ring)
+    return DUO_ERR_INVALID;
+  PrefillRun r[kPrefillMaxRuns];
+  *nruns = prefill_runs(retrieval == 1, len, n, r0, npos, S, W, r);
+  for (int i = 0; i < *nruns; ++i) {
+    runs[i][0] = r[i].src;
+    runs[i][1] = r[i].first;
+    runs[i][2] = r[i].count;
+  }
+  const PrefillRing v = prefill_ring(len + r0, len, S, W);
+  ring[0] = v.lo1;
+  ring[1] = v.hi1;
+  ring[2] = v.lo2;
+  ring[3] = v.hi2;
+  return DUO_OK;
+}
+
+extern "C" duo_status duo_debug_prefill_deal(int nitems, const int *tiles, const int *tile_cost, int sms, int *whole,
+                                             int *ctas, int (*shares)[4], int (*cuts)[4], int *ncuts) {
+  if (nitems < 1 || !tiles || !tile_cost || sms < 1 || !whole || !ctas || !shares || !cuts || !ncuts)
+    return DUO_ERR_INVALID;
+  for (int i = 0; i < nitems; ++i)
+    if (tiles[i] < 1 || tile_cost[i] < 1 || tiles[i] > (1 << 24) || tile_cost[i] > 64) return DUO_ERR_INVALID;
+  try {
+    std::vector<Item> items(nitems);
+    for (int i = 0; i < nitems; ++i) items[i] = {tiles[i], tile_cost[i]};
+    Deal deal;
+    deal_items(items, sms, &deal);
+    *whole = deal.whole;
+    *ctas = deal.ctas;
+    *ncuts = static_cast<int>(deal.cuts.size());
+    for (int c = 0; c < deal.ctas; ++c) {
+      const PrefillShare &s = deal.share[c];
+      shares[c][0] = s.item;
+      shares[c][1] = s.tile;
+      shares[c][2] = s.tiles;
+      shares[c][3] = s.part;
+    }
+    for (int i = 0; i < *ncuts; ++i) {
+      const Deal::Cut &x = deal.cuts[i];
+      cuts[i][0] = x.item;
+      cuts[i][1] = x.pieces;
+      cuts[i][2] = x.part0;
+      cuts[i][3] = x.part1;
+    }
+  } catch (const std::exception &) {  // out of host memory
+    return DUO_ERR_INVALID;
+  }
+  return DUO_OK;
+}

@@ -85,6 +85,11 @@ def lib() -> ctypes.CDLL:
             L.duo_debug_launch_controls.argtypes = [i32, i64]
             L.duo_debug_device_stall.restype = i32
             L.duo_debug_device_stall.argtypes = [i32]
+            i32p = ctypes.POINTER(i32)
+            L.duo_debug_prefill_runs.restype = i32
+            L.duo_debug_prefill_runs.argtypes = [i32] * 7 + [vp, i32p, vp]
+            L.duo_debug_prefill_deal.restype = i32
+            L.duo_debug_prefill_deal.argtypes = [i32, vp, vp, i32, i32p, i32p, vp, vp, i32p]
             L.duo_pool_bytes.restype = ctypes.c_size_t
             L.duo_pool_bytes.argtypes = [i32, i32, i32, vp, i32, i32, i32, i64, i64, ctypes.POINTER(duo_opts)]
             L.duo_pool_create.restype = i32
@@ -342,6 +347,24 @@ def duo_pool_region(handle, layer, which):
 
 def duo_pool_device_status(handle, stream=None) -> int:
     return lib().duo_pool_device_status(handle, _ptr(stream))
+
+
+def duo_debug_prefill_runs(retrieval, length, n, r0, npos, S, W):
+    """Returns (status, [(source, first tile, tiles)], ring [4])."""
+    runs, count, ring = (ctypes.c_int * 15)(), ctypes.c_int(), (ctypes.c_int * 4)()
+    st = lib().duo_debug_prefill_runs(retrieval, length, n, r0, npos, S, W, runs, ctypes.byref(count), ring)
+    return st, [tuple(runs[3 * i:3 * i + 3]) for i in range(count.value)], list(ring)
+
+
+def duo_debug_prefill_deal(tiles, tile_cost, sms):
+    """Returns (status, whole, ctas, shares, cuts), both of them lists of four numbers."""
+    ints = ctypes.c_int * len(tiles)
+    whole, ctas, count = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    shares, cuts = (ctypes.c_int * (4 * 148))(), (ctypes.c_int * (4 * 148))()
+    st = lib().duo_debug_prefill_deal(len(tiles), ints(*tiles), ints(*tile_cost), sms, ctypes.byref(whole),
+                                      ctypes.byref(ctas), shares, cuts, ctypes.byref(count))
+    rows = lambda a, m: [tuple(a[4 * i:4 * i + 4]) for i in range(m)]  # noqa: E731
+    return st, whole.value, ctas.value, rows(shares, ctas.value), rows(cuts, count.value)
 
 
 # ---- torch-owned cache ----

@@ -485,6 +485,24 @@ DUO_API duo_status duo_debug_launch_controls(int dry_run, int64_t fail_after);
  */
 DUO_API duo_status duo_debug_device_stall(int on);
 
+/*
+ * Read-back of how duo_pool_prefill shares its work out (host only, nothing is launched;
+ * tests only).
+ * duo_debug_prefill_runs: the key tiles (of 128) of the two query tiles, npos positions each, that
+ *   start at position r0 of n new tokens behind len cached ones, for a retrieval (1) or a
+ *   streaming (0) head: runs[i] = {source, first tile, tiles}, source 0 the sequence's pages, 1
+ *   its sink and ring slots, 2 the call's rows; ring = {lo, hi, lo, hi}, the ring slots that
+ *   query r0 sees.  runs has room for 5.
+ * duo_debug_prefill_deal: items with tiles[i] >= 1 key tiles of cost tile_cost[i] >= 1 each on at
+ *   most 148 CTAs, no more than sms: CTA c takes items c, c + ctas, ... below *whole, then
+ *   shares[c] = {item, tile, tiles, place}; cuts[i] = {item, pieces, place of the first, of the
+ *   second; two places on for each one more}.  shares and cuts have room for 148.
+ */
+DUO_API duo_status duo_debug_prefill_runs(int retrieval, int len, int n, int r0, int npos, int S, int W,
+                                          int (*runs)[3], int *nruns, int ring[4]);
+DUO_API duo_status duo_debug_prefill_deal(int nitems, const int *tiles, const int *tile_cost, int sms, int *whole,
+                                          int *ctas, int (*shares)[4], int (*cuts)[4], int *ncuts);
+
 /* Static description of a status code. */
 DUO_API const char *duo_status_str(duo_status status);
 
