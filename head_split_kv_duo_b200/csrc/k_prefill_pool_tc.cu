@@ -597,6 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
           const float tmax = largest(v) * scale;
           const bool need = tmax > m + kSlack;
           if (!__any_sync(0xffffffffu, need)) break;
+          // stores land in no order: these weights before the ones that go over them.  (Here: the
+          // same wait behind the loop below made long calls 3 to 6 % slower, 2.59 for 2.51 M
+          // cycles, 8192 tokens on 24576, by how the compiler laid it out.)
+          tc::st_wait();
           const float a = need ? ex2(m - tmax) : 1.f;  // 0 while m is -inf
           if (need) m = tmax;
           alpha *= a;
@@ -609,7 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_pool_kernel(const __grid_
             for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(x[e] * a);
             tc::st16(o_cols + 16 * q, u);
           }
-          tc::st_wait();  // stores are in no order: the first weights land before the second are stored over them
         }
         tc::st_wait();
         tc::fence_before();

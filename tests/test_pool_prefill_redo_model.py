@@ -45,13 +45,13 @@ def warp(sim, redone, wait_between=True, wait_before_rest=True):
                 yield None
             if redo:
                 ref += 1
+                if wait_between:
+                    yield from all_landed()
                 for b in range(OPARTS):
                     if j > 0:
                         sim.read(f"o{b}", ("product", j - 1))
                     store(f"o{b}", ("rescaled", j, ref))
                     yield None
-                if wait_between:
-                    yield from all_landed()
                 for b in range(EARLY):
                     store(f"p{b}", (j, ref))
                     yield None
