@@ -69,6 +69,11 @@ constexpr int kPrefillParts = 2 * kPrefillCtas;  // pieces of cut items: a CTA's
 // [2 tiles][33 groups of four][128 rows][4]: the rows' threads write and read side by side.
 constexpr int kPrefillRow = 132;
 constexpr int kPrefillMaxRuns = 5;
+// Longest piece of a CTA, in key tiles.  A role may wait while others work through a piece (the
+// lister for a free place: one piece; the second query tile's softmax, of pieces that have one
+// query tile: the four listed), and waits give up after 2 s.  A tile takes 1.9 us (of one
+// query tile 1.6 us): 0.25 s and 0.84 s, less than 2 s at half the clock.
+constexpr int kPrefillMaxPiece = 1 << 17;
 
 // Where an item's key tiles come from: the sequence's pages, its sinks and ring in slot
 // order, the call's own rows.

@@ -293,6 +293,21 @@ void deal_items(const std::vector<Item> &items, int sms, Deal *d) {
   }
 }
 
+// Key tiles of the longest piece that a CTA works through.
+int longest_piece(const std::vector<Item> &items, const Deal &d) {
+  int longest = 0;
+  for (int u = 0; u < d.whole; ++u) longest = std::max(longest, items[u].tiles);
+  for (const PrefillShare &s : d.share) {
+    int u = s.item, tile = s.tile;
+    for (int left = s.tiles; left > 0; tile = 0, ++u) {
+      const int nt = std::min(items[u].tiles - tile, left);
+      longest = std::max(longest, nt);
+      left -= nt;
+    }
+  }
+  return longest;
+}
+
 duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int *n, const void *q, const void *k,
                    const void *v, void *out, float *lse, cudaStream_t st) {
   std::vector<uint8_t> seen(P->max_seqs, 0);
@@ -405,6 +420,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   a.retr_items = a.lists.rfirst[nseq];
   Deal deal;
   deal_items(items, P->num_sms, &deal);
+  if (longest_piece(items, deal) > kPrefillMaxPiece) return DUO_ERR_UNSUPPORTED;
   a.whole_items = deal.whole;
   a.ctas = deal.ctas;
   std::copy(deal.share.begin(), deal.share.end(), a.lists.share);

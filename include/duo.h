@@ -335,7 +335,9 @@ DUO_API duo_status duo_pool_append_kv(duo_pool *pool, int layer, int seq, const 
  * some rows are split over CTAs, with partial rows in the pool's scratch: results repeat
  * bit for bit for the same lengths and counts), then one that joins split rows and appends.
  * nseq <= 128, at most 262144 tokens (else DUO_ERR_INVALID).  DUO_ERR_CAPACITY past max_len
- * or without free pages; on any error the cache is unchanged.
+ * or without free pages.  DUO_ERR_UNSUPPORTED when one CTA would have to read more than
+ * 16777216 keys of a head in one go, which takes many tokens on a history longer than that:
+ * calls of fewer tokens split such a history over CTAs.  On any error the cache is unchanged.
  */
 DUO_API duo_status duo_pool_prefill(duo_pool *pool, int layer, int nseq, const int *seqs, const int *n, const void *q,
                                     const void *k, const void *v, void *out, float *lse, void *cuda_stream);
