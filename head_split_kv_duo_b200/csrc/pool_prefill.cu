@@ -293,19 +293,20 @@ void deal_items(const std::vector<Item> &items, int sms, Deal *d) {
   }
 }
 
-// Key tiles of the longest piece that a CTA works through.
-int longest_piece(const std::vector<Item> &items, const Deal &d) {
-  int longest = 0;
-  for (int u = 0; u < d.whole; ++u) longest = std::max(longest, items[u].tiles);
+// Does every CTA's every piece end before waits do?
+bool pieces_fit(const std::vector<Item> &items, const Deal &d) {
+  auto fits = [](const Item &i) { return i.tiles <= kPrefillMaxPiece; };
+  if (std::all_of(items.begin(), items.end(), fits)) return true;
+  if (!std::all_of(items.begin(), items.begin() + d.whole, fits)) return false;
   for (const PrefillShare &s : d.share) {
     int u = s.item, tile = s.tile;
     for (int left = s.tiles; left > 0; tile = 0, ++u) {
       const int nt = std::min(items[u].tiles - tile, left);
-      longest = std::max(longest, nt);
+      if (nt > kPrefillMaxPiece) return false;
       left -= nt;
     }
   }
-  return longest;
+  return true;
 }
 
 duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int *n, const void *q, const void *k,
@@ -420,7 +421,7 @@ duo_status prefill(duo_pool *P, int layer, int nseq, const int *seqs, const int 
   a.retr_items = a.lists.rfirst[nseq];
   Deal deal;
   deal_items(items, P->num_sms, &deal);
-  if (longest_piece(items, deal) > kPrefillMaxPiece) return DUO_ERR_UNSUPPORTED;
+  if (!pieces_fit(items, deal)) return DUO_ERR_UNSUPPORTED;
   a.whole_items = deal.whole;
   a.ctas = deal.ctas;
   std::copy(deal.share.begin(), deal.share.end(), a.lists.share);
