@@ -24,11 +24,12 @@
 // through shared memory, and keep them in registers, multiplied by the weights, for all
 // of the token's query rows and again for its keys: a pair costs two products, two fused
 // multiply-adds and the scaling, on packed fp32 pairs.
-// 32768 tokens of 32 + 8 + 8 heads, bf16: 141 us, 5.7 TB/s, 87 % of the copy rate.  What
-// it took: the factors in registers for 190 -> 156 us (before, each row unpacked its
-// weights again and multiplied by them and by cos and sin in turn); blocks of two warps,
-// 128 rows in flight per SM at 112 registers, -> 141 us (256 threads: 164; three
-// or four groups per warp: 150 to 162; registers capped for more warps: 145 to 166).
+// 32768 tokens of 32 + 8 + 8 heads, bf16: 141 us alone, 5.7 TB/s, 87 % of the copy rate (136
+// back to back).  What it took: the factors in registers for 190 -> 156 us (before, each row
+// unpacked its weights again and multiplied by them and by cos and sin in turn); blocks of
+// two warps, ten of them and 160 rows in flight per SM at 96 registers (interleaved pairs:
+// 103 and nine), -> 141 us (256 threads: 164; three or four groups per warp: 150 to 162;
+// registers capped for more warps: 145 to 166).
 #include <cmath>
 #include <new>
 

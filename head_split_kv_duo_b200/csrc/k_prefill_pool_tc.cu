@@ -37,20 +37,20 @@
 // drains and exits.
 //
 // Bound: a pair of tiles (256 rows x 128 keys) costs 2048 cycles of the tensor core and as
-// many of MUFU (exponentials of two warps per scheduler); it takes about 2650, and long
-// calls run at the power limit (1.66 GHz).  8 KV heads (4 of them retrieval heads) of 4
-// query heads, alone on the GPU with the append:
-//   8192 tokens on 24576: 1.51 ms, 1.30 PFLOP/s (back to back, at 1.45 GHz, 1.71 ms)
-//   64 tokens on 131000: 72 us with a fork (0.27 GB and 69 GFLOP: 41 us at either rate)
-// Steps from a first version of 1.89 ms and 84 us (one CTA per item, the maximum before the
-// exponentials, P handed over whole, lane 0 alone issuing), in that order:
+// many of MUFU (exponentials of two warps per scheduler); it takes 3120 with every SM at
+// work (one query tile of 128 rows: 2740), a piece 7400 more, and long calls run at the
+// power limit.  8 KV heads (4 of them retrieval heads) of 4 query heads, fork and append included:
+//   8192 tokens on 24576: alone 1.51 ms (1.67 GHz), 1.30 PFLOP/s; back to back 1.74 ms, 1.13
+//   64 tokens on 131000, back to back: 73 us (0.27 GB and 69 GFLOP: 41 us at either rate)
+// Steps from a first version of 1.89 ms and 96 us (one CTA per item, the maximum before the
+// exponentials, P handed over whole, lane 0 alone issuing), in that order, each pass alone:
 //   products of a tile's first 96 keys start before the other 32 are done, the maximum is
 //   checked beside the exponentials, K and V are waited for before P, the issuing warp runs
 //   on uniform values (issue 3700 -> 2000 cycles a pair of tiles): 1.61 ms
 //   rows out through shared memory, partial rows transposed, masks as two runs: 1.55 ms
 //   one site each for listing and storing (84 -> 75 KB of code: the loops then stay in the
 //   instruction cache): 1.51 ms
-//   even shares by cost: 630 -> 330 us for eight sequences of very different lengths
+//   even shares by cost: 630 -> 340 us for eight sequences of very different lengths
 // Without gain: part of the exponentials as polynomials on the FMA pipe (1.55 to 1.76 ms for
 // an eighth to a third of them), P in halves (1.65) or whole (1.54), tiles fetched into L2
 // ahead of their loads (73 -> 85 us), listing pieces with a function call.
@@ -196,8 +196,11 @@ __device__ __forceinline__ float largest(const float (&v)[128]) {
 }
 
 // P = exp2(c v - mc) of logits v[32 B .. 32 B + 32) as bf16 pairs into columns 16 B .. of
-// `cols` (not waited for); returns their fp32 sum.  P is rounded to bf16 for the tensor
-// core (2^-9 relative, of random sign over a row); the sum takes the unrounded values.
+// `cols` (not waited for); returns their fp32 sum.  P is rounded to bf16 for the tensor core,
+// which takes both operands in one type, V's: half a step, 2^-8 relative at most, of random
+// sign over a row.  With the output's own rounding that is 2.2e-3 of the result's norm
+// against 64 bits, where a P of 32 bits leaves 1.7e-3; P as two bf16 parts would cost a
+// second product.  The sum takes the unrounded values, and lse is that of 32 bits.
 template <int B>
 __device__ __forceinline__ float probabilities(const float (&v)[128], float c, float mc, uint32_t cols) {
   const uint64_t cc = pack2(c, c), mm = pack2(-mc, -mc);

@@ -19,7 +19,9 @@ struct duo_pool {
   int num_sms = 0;
   uint32_t *status = nullptr;
   uint32_t *counters = nullptr;  // one ticket per item of a call
-  float *partials = nullptr;     // (max CTAs + items) segments of G partial rows
+  // (max CTAs + items) segments of G partial rows of a decode step, or the pieces of a
+  // pre-fill (40 MB, the larger for most pools)
+  float *partials = nullptr;
   int max_items = 0;
   duo::PoolLayerDesc *d_layers = nullptr;
   int *d_table = nullptr;

@@ -8,7 +8,7 @@
 //
 // The last launch is bound by latency when it is short (4 to 5 us: parameters, partial
 // rows, stores, one after the other) and by the partial rows otherwise: 8192 tokens on
-// 24576, 40 MB of them and 33 MB of k and v in, 17 MB of rows out, 18 us.
+// 24576, 28 MB of them and 33 MB of k and v in, 17 MB of rows out, 18 us.
 #include <cmath>
 #include <exception>
 
@@ -225,10 +225,14 @@ __global__ void __launch_bounds__(256, 3) pool_prefill_finish_kernel(const __gri
 // Deals the items out: whole ones in rounds, item r * ctas + c to CTA c, as long as no CTA
 // gets more than its even share of the cost, so that neighbours read the same keys at about
 // the same time; then the rest, cut where a CTA's share is full.  Costs are in quarters of a
-// retrieval head's key tile (2650 cycles): a streaming head's tile, masked for the most part,
-// is five, and a piece sixteen more than its tiles (queries, the first product, masks at
-// its ends, the rows' way out).  A short call runs on as many CTAs as it has tiles (calls of
-// 20 to 100 us with their forks: 6 % shorter than with two tiles or more for each).
+// retrieval head's key tile (3120 cycles with every SM at work): a streaming head's tile,
+// masked for the most part, is five (3250 to 3780 cycles by the window), and a piece sixteen
+// more than its tiles.  A whole piece between others measures 7400 cycles beside its tiles
+// (queries, the first product, masks at its ends, the rows' way out), which would be ten; a
+// cut one also leaves partial rows, which the last launch reads again.  A short call is
+// launched on as many CTAs as it has tiles (calls of 20 to 100 us with their forks: 6 %
+// shorter than with two tiles or more for each); shares grow in steps until everything is
+// dealt, so some of them may stay without work (4 x 5 tokens: 128 of 148 have some).
 struct Item {
   int tiles, tile_cost;
 };

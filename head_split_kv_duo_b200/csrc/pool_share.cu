@@ -13,8 +13,9 @@
 // with two or four 16-byte loads each in flight, so a fork of one child is a single wave of
 // loads over the GPU, and many pieces stream at the copy bandwidth of HBM.  4 retrieval
 // and 4 streaming heads, S + W = 528: one child of 333 tokens on 4 layers 3.3 us (its
-// launch), eight of 4200 tokens on 8 layers 15.5 us (93 MB, 14 us at the copy bandwidth),
-// a copy of 32900 tokens on 8 layers 167 us (6.6 TB/s, 100 % of it).
+// launch), eight of 4200 tokens on 8 layers 15.8 us (93 MB, 14 us at the copy bandwidth),
+// a copy of 32900 tokens on 8 layers 167 us (6.6 TB/s, 100 % of it).  Figures in this file:
+// mean of ten calls back to back in a captured graph, without the host.
 #include "device_common.cuh"
 #include "nvtx_range.h"
 #include "pool_internal.h"
@@ -106,8 +107,8 @@ __global__ void __launch_bounds__(256) pool_share_kernel(const __grid_constant__
 }
 
 // Gives `n` free slots of Q the contents of sequence `seq` of P: the first `shared` pages
-// by reference (P == Q), the others and the rings as copies.  Slots and pages are taken
-// only when every launch was accepted.
+// by reference (P == Q), the others and the rings as copies.  Pages are taken before the first
+// launch, as it lists them, and go back if one fails; slots are taken when all were accepted.
 duo_status share_sequence(const duo_pool *P, int seq, duo_pool *Q, int shared, int n, cudaStream_t st, int *out) {
   const std::vector<int> &src = P->pages[seq];
   const std::vector<int64_t> &lens = P->len[seq];
@@ -163,9 +164,9 @@ duo_status share_sequence(const duo_pool *P, int seq, duo_pool *Q, int shared, i
       c.pieces = std::max({c.npages * (kPoolTile / rows), ring, 1});
       return static_cast<int64_t>(P->layers) * c.heads2 * c.pieces;
     };
-    // 64 rows a piece stream best (32900 tokens of 8 layers 170 us, 197 with 32); where that
+    // 64 rows a piece stream best (32900 tokens of 8 layers 167 us, 200 with 32); where that
     // is less than twice what the GPU holds at once, pieces of 32 share the work more
-    // evenly (eight children of 4200 tokens 22.5 us for 24.6)
+    // evenly (eight children of 4200 tokens 15.8 us for 17.5, one of 333 tokens 3.5 for 3.9)
     constexpr int64_t kFew = 2 * 8 * 148;
     const bool few = blocks(64) < kFew;
     const int64_t grid = blocks(few ? 32 : 64);

@@ -290,7 +290,9 @@ DUO_API duo_status duo_decode_attention_static_scratch(duo_cache *cache, int lay
 typedef struct duo_pool duo_pool;
 
 /* Bytes of the pool buffer: max_seqs sequence slots, num_pages pages per layer, every
- * sequence at most max_len tokens.  0 for invalid arguments. */
+ * sequence at most max_len tokens, and scratch for the partial rows of one call: at least
+ * the 40 MB that duo_pool_prefill may need, whether or not the pool is pre-filled.  0 for
+ * invalid arguments. */
 DUO_API size_t duo_pool_bytes(int layers, int kv_heads, int head_dim, const uint8_t *retrieval_head_mask, int S, int W,
                               int max_seqs, int64_t max_len, int64_t num_pages, const duo_opts *opts);
 
@@ -327,6 +329,9 @@ DUO_API duo_status duo_pool_append_kv(duo_pool *pool, int layer, int seq, const 
  * drafts to be checked and single tokens; sequences of a fork read their shared pages.
  *   q, out  device [tokens][Hq][d];  k, v  device [tokens][Hkv][d], the tokens of seqs[0],
  *           then those of seqs[1], ... (tokens = sum of n[i]);  lse [tokens][Hq] fp32, or NULL
+ * Logits, softmax sums, partial rows and lse are fp32; the softmax weights are rounded to
+ * bf16 for their product with v, as in duo_prefill_chunk (in all 2.2e-3 of the result's norm
+ * from exact, where the rounding of out alone is 1.7e-3).
  * A sequence's results do not depend on the other sequences' values.  Within a sequence k
  * and v must be finite: a row that is not spoils queries that do not see it too.
  * All but lse 16-byte aligned; out and lse overlap neither the inputs nor one another nor the
