@@ -285,7 +285,7 @@ DUO_API duo_status duo_decode_attention_static_scratch(duo_cache *cache, int lay
  * (and where tokens went into a ring, a second replay starts from the ring as the first
  * left it).
  * Errors follow the cache's contract: checked before any launch, lengths follow what the
- * cache holds.
+ * cache holds.  A call that runs out of host memory is DUO_ERR_INVALID and changes nothing.
  */
 typedef struct duo_pool duo_pool;
 
